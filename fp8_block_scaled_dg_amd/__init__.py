@@ -14,6 +14,11 @@ article, deepseek.csdn.net, section 4.2 "advanced tuning"):
 * ``quantize_fp8_1x128(x, codes=None, sf=None)``: activations -> (A codes, sfA)
 * ``m_grouped_fp8_gemm_nt_{contiguous,masked}_swiglu(...)``: Linear1 with a fused
   SwiGLU + requantization epilogue -> (codes, sf) of h = silu(gate) * up
+* ``rmsnorm_fp8_1x128(x, weight, eps, residual=...)``: RMS norm of x + residual ->
+  (A codes, sfA); ``rmsnorm_backward``: its gradients
+* ``fp8_gemm_nt_bias_act(a, b, c, a_sf, b_sf, bias, activation, residual)`` and
+  ``fp8_gemm_nt_bias_act_fp8(...)`` -> (codes, sf): the dense GEMM with its epilogue;
+  ``bias_act_backward_fp8``: the epilogue's gradients
 
 Operands: ``a``/``b`` are ``torch.float8_e4m3fn`` (``torch.uint8`` holding e4m3fn
 codes is accepted too), ``a_sf``/``b_sf`` ``torch.float32``, ``c`` ``torch.bfloat16``
@@ -94,6 +99,20 @@ for _name in ("dg_fp8_gemm_nn", "dg_fp8_gemm_tn", "dg_fp8_gemm_tt"):
 lib.dg_quantize_fp8_1x128.restype = ctypes.c_int
 lib.dg_quantize_fp8_1x128.argtypes = [_vp, _i32, _vp, _vp, _i64, _i64, _vp]
 
+lib.dg_rmsnorm_fp8_1x128.restype = ctypes.c_int
+lib.dg_rmsnorm_fp8_1x128.argtypes = [_vp, _vp, _i32, _vp, _i32, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                     _i32, _i64, _i64, _vp]
+lib.dg_rmsnorm_backward.restype = ctypes.c_int
+lib.dg_rmsnorm_backward.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _vp]
+lib.dg_fp8_gemm_nt_bias_act.restype = ctypes.c_int
+lib.dg_fp8_gemm_nt_bias_act.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp,
+                                        _i64, _i64, _i64, _vp]
+lib.dg_fp8_gemm_nt_bias_act_fp8.restype = ctypes.c_int
+lib.dg_fp8_gemm_nt_bias_act_fp8.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32,
+                                            _i32, _vp, _i64, _i64, _i64, _vp]
+lib.dg_bias_act_backward_fp8.restype = ctypes.c_int
+lib.dg_bias_act_backward_fp8.argtypes = [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i64, _i64, _vp]
+
 lib.dg_release_workspaces.restype = ctypes.c_int
 lib.dg_release_workspaces.argtypes = []
 lib.dg_num_configs.restype = _i32
@@ -103,6 +122,7 @@ lib.dg_config_name.argtypes = [_i32]
 
 KIND_DENSE, KIND_CONTIGUOUS, KIND_MASKED = 0, 1, 2
 DTYPE_F32, DTYPE_BF16 = 0, 1
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 BLOCK = 128
 
 
@@ -352,6 +372,181 @@ def quantize_fp8_1x128(x, codes=None, sf=None):
     return codes, sf
 
 
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return d
+
+
+def _act(activation) -> int:
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    return code
+
+
+def _fp8_outputs(M: int, N: int, codes, sf, ue8m0: bool, dev):
+    """(codes, sf, packed?) of an FP8 output [M, N]: new tensors where none is passed. The
+    dtype of a passed sf (float32, or int32 for packed UE8M0) says its form."""
+    if codes is None:
+        codes = torch.empty((M, N), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _fp8(codes, "codes")
+        _need(codes, "codes", codes.dtype, (M, N), dev)
+    if sf is None:
+        sf = (torch.empty((M, (N // BLOCK + 3) // 4), dtype=torch.int32, device=dev) if ue8m0 else
+              torch.empty((M, N // BLOCK), dtype=torch.float32, device=dev))
+        return codes, sf, ue8m0
+    if sf.dtype == torch.int32:
+        _need(sf, "sf", torch.int32, (M, (N // BLOCK + 3) // 4), dev)
+        return codes, sf, True
+    _need(sf, "sf", torch.float32, (M, N // BLOCK), dev)
+    return codes, sf, False
+
+
+def rmsnorm_fp8_1x128(x, weight, eps=1e-6, residual=None, h=None, rstd=None, codes=None, sf=None,
+                      ue8m0=False):
+    """RMS norm of x + residual ([M, K] float32 or bfloat16) with weight [K], quantized per
+    1x128 block: returns (codes [M, K] e4m3fn, sf), the a and a_sf of the GEMM calls. sf is
+    fp32 [M, K/128], or int32 [M, ceil(K/512)] packed UE8M0 (ue8m0=True, or a passed sf of
+    that dtype). h, when passed, receives x + residual (it may be x or residual itself),
+    rstd (fp32 [M]) 1 / rms; rmsnorm_backward takes both."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    dtype = _float_type(x, "x")
+    M, K = x.shape
+    dev = x.device
+    _dev(x, "x", dev)
+    w_dtype = _float_type(weight, "weight")
+    _need(weight, "weight", weight.dtype, (K,), dev)
+    if residual is not None:
+        _need(residual, "residual", x.dtype, (M, K), dev)
+    if h is not None:
+        _need(h, "h", x.dtype, (M, K), dev)
+    if rstd is not None:
+        _need(rstd, "rstd", torch.float32, (M,), dev)
+    codes, sf, packed = _fp8_outputs(M, K, codes, sf, ue8m0, dev)
+    _run(dev, lib.dg_rmsnorm_fp8_1x128, x.data_ptr(), residual.data_ptr() if residual is not None else None,
+         dtype, weight.data_ptr(), w_dtype, eps, h.data_ptr() if h is not None else None,
+         rstd.data_ptr() if rstd is not None else None, codes.data_ptr(), sf.data_ptr(), packed, M, K)
+    return codes, sf
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None):
+    """Gradients of rmsnorm_fp8_1x128 (the quantization taken as the identity), from the h
+    and rstd it stored: returns (dx [M, K] of h's dtype, dweight [K] float32). dh, the
+    gradient that reaches h along the residual stream, is added to dx; dx is the gradient
+    of x and of residual alike, and may be dy, dh or h itself."""
+    if h.dim() != 2:
+        raise ValueError("h must be [M, K]")
+    dtype = _float_type(h, "h")
+    M, K = h.shape
+    dev = h.device
+    _dev(h, "h", dev)
+    _need(dy, "dy", h.dtype, (M, K), dev)
+    w_dtype = _float_type(weight, "weight")
+    _need(weight, "weight", weight.dtype, (K,), dev)
+    _need(rstd, "rstd", torch.float32, (M,), dev)
+    if dh is not None:
+        _need(dh, "dh", h.dtype, (M, K), dev)
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _need(dx, "dx", h.dtype, (M, K), dev)
+    if dweight is None:
+        dweight = torch.empty((K,), dtype=torch.float32, device=dev)
+    else:
+        _need(dweight, "dweight", torch.float32, (K,), dev)
+    _run(dev, lib.dg_rmsnorm_backward, dy.data_ptr(), dh.data_ptr() if dh is not None else None,
+         h.data_ptr(), dtype, weight.data_ptr(), w_dtype, rstd.data_ptr(), dx.data_ptr(),
+         dweight.data_ptr(), M, K)
+    return dx, dweight
+
+
+def _bias_act_operands(a, b, a_sf, b_sf, bias, pre):
+    """Checks what the two epilogue GEMMs share: (M, N, K, device, packed a_sf?, bias pointer,
+    bias dtype, pre pointer)."""
+    _fp8(a, "a"), _fp8(b, "b")
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b must be 2-D")
+    M, K = a.shape
+    N = b.shape[0]
+    dev = a.device
+    _dev(a, "a", dev)
+    _need(b, "b", b.dtype, (N, K), dev)
+    packed = _a_sf_layout(a_sf, (M,), K, dev)
+    _need(b_sf, "b_sf", torch.float32, ((N + BLOCK - 1) // BLOCK, K // BLOCK), dev)
+    bias_ptr, bias_dtype = None, 0
+    if bias is not None:
+        bias_dtype = _float_type(bias, "bias")
+        _need(bias, "bias", bias.dtype, (N,), dev)
+        bias_ptr = bias.data_ptr()
+    pre_ptr = None
+    if pre is not None:
+        _need(pre, "pre", torch.bfloat16, (M, N), dev)
+        pre_ptr = pre.data_ptr()
+    return M, N, K, dev, packed, bias_ptr, bias_dtype, pre_ptr
+
+
+def fp8_gemm_nt_bias_act(a, b, c, a_sf, b_sf, bias=None, activation=None, residual=None,
+                         pre=None) -> None:
+    """c [M, N] (bf16) = activation(a x b^T + bias) + residual, rounded once; writes c in
+    place. a, b and the scales as for fp8_gemm_nt; bias [N] float32 or bfloat16; activation
+    None, "relu", "silu", "gelu" or "gelu_tanh"; residual [M, N] bf16 (c itself is allowed);
+    pre, when passed, receives a x b^T + bias (bf16 [M, N], for bias_act_backward_fp8)."""
+    M, N, K, dev, packed, bias_ptr, bias_dtype, pre_ptr = _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
+    _need(c, "c", torch.bfloat16, (M, N), dev)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (M, N), dev)
+    _run(dev, lib.dg_fp8_gemm_nt_bias_act, a.data_ptr(), b.data_ptr(), c.data_ptr(), a_sf.data_ptr(),
+         packed, b_sf.data_ptr(), bias_ptr, bias_dtype, _act(activation),
+         residual.data_ptr() if residual is not None else None, pre_ptr, M, N, K)
+
+
+def fp8_gemm_nt_bias_act_fp8(a, b, a_sf, b_sf, bias=None, activation=None, pre=None, codes=None,
+                             sf=None, ue8m0=False):
+    """activation(a x b^T + bias) quantized per 1x128 block: returns (codes [M, N] e4m3fn,
+    sf), the next GEMM's a and a_sf (sf as in rmsnorm_fp8_1x128). N % 128 == 0; the other
+    arguments as for fp8_gemm_nt_bias_act."""
+    M, N, K, dev, packed, bias_ptr, bias_dtype, pre_ptr = _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
+    codes, sf, sf_packed = _fp8_outputs(M, N, codes, sf, ue8m0, dev)
+    _run(dev, lib.dg_fp8_gemm_nt_bias_act_fp8, a.data_ptr(), b.data_ptr(), codes.data_ptr(),
+         sf.data_ptr(), sf_packed, a_sf.data_ptr(), packed, b_sf.data_ptr(), bias_ptr, bias_dtype,
+         _act(activation), pre_ptr, M, N, K)
+    return codes, sf
+
+
+def bias_act_backward_fp8(dc, pre=None, activation=None, codes=None, sf=None, dbias=None,
+                          need_dbias=True, ue8m0=False):
+    """Backward of the bias + activation epilogue: p = dc * activation'(pre) (dc, pre bf16
+    [M, N]; pre may be None without an activation), returned as (codes, sf, dbias): p
+    quantized per 1x128 block and dbias [N] float32 = p summed over rows (None with
+    need_dbias=False). The input's gradient is then fp8_gemm_nn(codes, b, da, sf,
+    b_sf.t().contiguous()) with the forward call's b."""
+    if dc.dim() != 2:
+        raise ValueError("dc must be [M, N]")
+    M, N = dc.shape
+    dev = dc.device
+    _dev(dc, "dc", dev)
+    _need(dc, "dc", torch.bfloat16, (M, N), dev)
+    act = _act(activation)
+    if pre is not None:
+        _need(pre, "pre", torch.bfloat16, (M, N), dev)
+    codes, sf, packed = _fp8_outputs(M, N, codes, sf, ue8m0, dev)
+    if dbias is not None:
+        _need(dbias, "dbias", torch.float32, (N,), dev)
+    elif need_dbias:
+        dbias = torch.empty((N,), dtype=torch.float32, device=dev)
+    _run(dev, lib.dg_bias_act_backward_fp8, dc.data_ptr(), pre.data_ptr() if pre is not None else None,
+         act, codes.data_ptr(), sf.data_ptr(), packed, dbias.data_ptr() if dbias is not None else None,
+         M, N)
+    return codes, sf, dbias
+
+
 def release_workspaces() -> None:
     """Free the library's own device buffers (split-K partials and counters, transposed
     operand copies) after the devices holding them go idle. No HIP graph holding a
@@ -371,4 +566,5 @@ def config_names() -> list[str]:
 
 __all__ = ["config_names", "fp8_gemm_nt", "fp8_gemm_nn", "fp8_gemm_tn", "fp8_gemm_tt", "m_grouped_fp8_gemm_nt_contiguous", "m_grouped_fp8_gemm_nt_masked",
            "m_grouped_fp8_gemm_nt_contiguous_swiglu", "m_grouped_fp8_gemm_nt_masked_swiglu",
-           "quantize_fp8_1x128", "describe_config", "release_workspaces", "BUILD_ID", "DGError", "lib", "LIB_PATH"]
+           "quantize_fp8_1x128", "rmsnorm_fp8_1x128", "rmsnorm_backward", "fp8_gemm_nt_bias_act",
+           "fp8_gemm_nt_bias_act_fp8", "bias_act_backward_fp8", "ACTIVATIONS", "describe_config", "release_workspaces", "BUILD_ID", "DGError", "lib", "LIB_PATH"]

@@ -1,0 +1,96 @@
+// activation.hpp -- the activations of the GEMM epilogue and their derivatives, in fp32.
+//
+//   relu(x)      = max(x, 0)                      relu'(x) = x > 0
+//   silu(x)      = x s(x), s(x) = 1 / (1 + e^-x)  silu'(x) = s (1 + x (1 - s))
+//   gelu(x)      = x Phi(x), Phi the normal distribution function
+//                                                 gelu'(x) = Phi(x) + x e^(-x^2/2) / sqrt(2 pi)
+//   gelu_tanh(x) = x (1 + tanh u) / 2 = x s(2u), u = sqrt(2/pi) (x + 0.044715 x^3)
+//                                                 x' = s + x s (1 - s) 2 u'
+// Phi is formed as Phi(-z) = t P(t) e^(-z^2/2) / 2 for z = |x|, t = 1 / (1 + 0.2687 z):
+// t P(t) approximates e^(y^2) erfc(y), y = z / sqrt 2, with a polynomial of degree 8 fitted
+// by reweighted least squares to 2.1e-8 relative over y in [0, 12]. Both tails of gelu then
+// keep a relative accuracy of 5e-7 for |x| < 3 and 4e-6 for |x| < 13 (the rounding of x^2
+// in the exponent); 1 + erf(x / sqrt 2) would cancel to a few bits at x = -5, which a block
+// scaled by its own largest value would show. A NaN passes through all of them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/dg.h"
+
+namespace dg {
+
+// 1 / (1 + e^-x): the 1-ulp hardware reciprocal; 0 when e^-x overflows
+__device__ __forceinline__ float act_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + expf(-x));
+}
+
+// (Phi(-z), e^(-z^2/2)) for z = |x|
+__device__ __forceinline__ float2 act_normal_tail(float z) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.26870056986808777f, z, 1.f));
+  float p = 0.05904914811253548f;
+  p = __builtin_fmaf(p, t, -0.2626967430114746f);
+  p = __builtin_fmaf(p, t, 0.3647571802139282f);
+  p = __builtin_fmaf(p, t, -0.16253234446048737f);
+  p = __builtin_fmaf(p, t, 0.23080509901046753f);
+  p = __builtin_fmaf(p, t, 0.13829860091209412f);
+  p = __builtin_fmaf(p, t, 0.204002246260643f);
+  p = __builtin_fmaf(p, t, 0.2139049917459488f);
+  p = __builtin_fmaf(p, t, 0.2144118696451187f);
+  const float g = expf(-0.5f * z * z);
+  return make_float2(0.5f * t * p * g, g);
+}
+
+__device__ __forceinline__ float act_gelu_tanh_u(float x) {  // 2u
+  return 1.5957691216057308f * __builtin_fmaf(0.044715f * x * x, x, x);
+}
+
+template <int N>
+__device__ __forceinline__ void act_apply(float (&v)[N], int act) {
+  if (act == DG_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] <= 0.f ? 0.f : v[i];
+  } else if (act == DG_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= act_sigmoid(v[i]);
+  } else if (act == DG_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float q = act_normal_tail(fabsf(v[i])).x;
+      v[i] *= v[i] > 0.f ? 1.f - q : q;
+    }
+  } else if (act == DG_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= act_sigmoid(act_gelu_tanh_u(v[i]));
+  }
+}
+
+// d[i] *= act'(x[i])
+template <int N>
+__device__ __forceinline__ void act_backward(float (&d)[N], const float (&x)[N], int act) {
+  if (act == DG_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = x[i] <= 0.f ? 0.f : d[i];
+  } else if (act == DG_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = act_sigmoid(x[i]);
+      d[i] *= s * __builtin_fmaf(x[i], 1.f - s, 1.f);
+    }
+  } else if (act == DG_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 q = act_normal_tail(fabsf(x[i]));
+      d[i] *= __builtin_fmaf(x[i] * q.y, 0.3989422804014327f, x[i] > 0.f ? 1.f - q.x : q.x);
+    }
+  } else if (act == DG_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = act_sigmoid(act_gelu_tanh_u(x[i]));
+      const float du = 1.5957691216057308f * __builtin_fmaf(0.134145f * x[i], x[i], 1.f);
+      d[i] *= __builtin_fmaf(x[i] * s * (1.f - s), du, s);
+    }
+  }
+}
+
+}  // namespace dg

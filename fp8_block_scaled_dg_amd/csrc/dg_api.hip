@@ -9,6 +9,7 @@
 // compiled ahead of time and chosen from the shape on the host.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -21,7 +22,9 @@
 #include <vector>
 
 #include "../../include/dg.h"
+#include "epilogue.hpp"
 #include "gemm_kernel.hpp"
+#include "norm_kernel.hpp"
 #include "pipe_kernel.hpp"
 #include "quant_kernel.hpp"
 #include "skinny_kernel.hpp"
@@ -94,10 +97,12 @@ TailSplit pipe_tail_split(int64_t tiles, int64_t KB) {
   return t;
 }
 
-template <class Cfg, int KIND, int LAY = 0>
-dg_status launch_pipe(const Problem& p0, int64_t blocks, hipStream_t stream) {
+template <class Cfg, int KIND, int LAY, int EPI>
+dg_status launch_pipe_as(const Problem& p0, int64_t blocks, const Epilogue& ep,
+                         hipStream_t stream) {
   PipeArgs a{};
   a.p = p0;
+  a.ep = ep;
   Problem& p = a.p;
   p.tiles_m = (int32_t)((p.M + Cfg::BM - 1) / Cfg::BM);
   p.tiles_n = (int32_t)((p.N + Cfg::BN - 1) / Cfg::BN);
@@ -120,11 +125,16 @@ dg_status launch_pipe(const Problem& p0, int64_t blocks, hipStream_t stream) {
   }
   a.items = (int32_t)grid;
   const int64_t wgs = grid < kCUs ? grid : kCUs;  // persistent, one workgroup per CU
-  hipLaunchKernelGGL((pipe_kernel<Cfg, KIND, false, LAY>), dim3((unsigned)wgs), dim3(Cfg::NT), 0,
-                     stream, a);
+  hipLaunchKernelGGL((pipe_kernel<Cfg, KIND, false, LAY, EPI>), dim3((unsigned)wgs), dim3(Cfg::NT),
+                     0, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
   return DG_OK;
+}
+
+template <class Cfg, int KIND, int LAY = 0>
+dg_status launch_pipe(const Problem& p, int64_t blocks, hipStream_t stream) {
+  return launch_pipe_as<Cfg, KIND, LAY, kEpiNone>(p, blocks, Epilogue{}, stream);
 }
 
 using Pipe256x128 = PipeCfg<256, 128>;
@@ -350,24 +360,25 @@ int tile_group(int64_t tiles) {
   return 1;
 }
 
-template <class Cfg, int LAY = 0>
-dg_status launch_skinny(const Problem& p0, int64_t blocks, hipStream_t stream) {
-  (void)blocks;
+template <class Cfg, int LAY, int EPI>
+dg_status launch_skinny_as(const Problem& p0, const Epilogue& ep, hipStream_t stream) {
   if (LAY != 0 && p0.sfa_packed) return fail(DG_ERR_UNSUPPORTED_SHAPE, "packed sfA with MN-contiguous operands");
-  constexpr int lds_bytes = (LAY & kLayBN) ? Cfg::LDS_BYTES_BN : Cfg::LDS_BYTES;
+  constexpr int lds_slots = (LAY & kLayBN) ? Cfg::LDS_BYTES_BN : Cfg::LDS_BYTES;
+  constexpr int lds_bytes = EPI != kEpiNone && Cfg::LDS_EPI > lds_slots ? Cfg::LDS_EPI : lds_slots;
   static std::once_flag once;
   static hipError_t attr_err = hipSuccess;
   std::call_once(once, [] {
-    attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, false, LAY>,
+    attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, false, LAY, EPI>,
                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
     if (attr_err == hipSuccess && LAY == 0)
-      attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, true>,
+      attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, true, 0, EPI>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
   });
   if (attr_err != hipSuccess)
     return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(attr_err));
   SkinnyArgs a{};
   a.p = p0;
+  a.ep = ep;
   const int KB = (int)(p0.K / kKBlock);
   const int64_t tiles = (p0.N + Cfg::BN - 1) / Cfg::BN;
   // K splits: as many as keep the grid within one workgroup per CU (a grid slightly
@@ -395,17 +406,23 @@ dg_status launch_skinny(const Problem& p0, int64_t blocks, hipStream_t stream) {
     if (st != DG_OK) return st;
   }
   if (LAY != 0)
-    hipLaunchKernelGGL((skinny_kernel<Cfg, false, LAY>), dim3((unsigned)grid), dim3(Cfg::NT),
+    hipLaunchKernelGGL((skinny_kernel<Cfg, false, LAY, EPI>), dim3((unsigned)grid), dim3(Cfg::NT),
                        lds_bytes, stream, a);
   else if (p0.sfa_packed)
-    hipLaunchKernelGGL((skinny_kernel<Cfg, true>), dim3((unsigned)grid), dim3(Cfg::NT),
+    hipLaunchKernelGGL((skinny_kernel<Cfg, true, 0, EPI>), dim3((unsigned)grid), dim3(Cfg::NT),
                        lds_bytes, stream, a);
   else
-    hipLaunchKernelGGL((skinny_kernel<Cfg, false>), dim3((unsigned)grid), dim3(Cfg::NT),
+    hipLaunchKernelGGL((skinny_kernel<Cfg, false, 0, EPI>), dim3((unsigned)grid), dim3(Cfg::NT),
                        lds_bytes, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
   return DG_OK;
+}
+
+template <class Cfg, int LAY = 0>
+dg_status launch_skinny(const Problem& p, int64_t blocks, hipStream_t stream) {
+  (void)blocks;
+  return launch_skinny_as<Cfg, LAY, kEpiNone>(p, Epilogue{}, stream);
 }
 
 // ---------------------------------------------------------------- stream kernel
@@ -439,14 +456,14 @@ bool stream_fits(int64_t M, int64_t N, int64_t K) {
   return stream_plan<Cfg>(N, K).KS <= Cfg::D;
 }
 
-template <class Cfg, int LAY = 0>
-dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
-  (void)blocks;
+template <class Cfg, int LAY, int EPI>
+dg_status launch_stream_as(const Problem& p0, const Epilogue& ep, hipStream_t stream) {
   if (LAY != 0 && p0.sfa_packed) return fail(DG_ERR_UNSUPPORTED_SHAPE, "packed sfA with MN-contiguous operands");
   const StreamPlan pl = stream_plan<Cfg, LAY>(p0.N, p0.K);
   if (pl.KS > Cfg::D) return fail(DG_ERR_UNSUPPORTED_SHAPE, "K run %lld > %d", (long long)pl.KS, Cfg::D);
   StreamArgs a{};
   a.p = p0;
+  a.ep = ep;
   a.S = (int32_t)pl.S;
   a.KS = (int32_t)pl.KS;
   a.tiles = (int32_t)pl.tiles;
@@ -458,14 +475,20 @@ dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
     if (st != DG_OK) return st;
   }
   if (LAY != 0)
-    hipLaunchKernelGGL((stream_kernel<Cfg, false, LAY>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
+    hipLaunchKernelGGL((stream_kernel<Cfg, false, LAY, EPI>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
   else if (p0.sfa_packed)
-    hipLaunchKernelGGL((stream_kernel<Cfg, true>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
+    hipLaunchKernelGGL((stream_kernel<Cfg, true, 0, EPI>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
   else
-    hipLaunchKernelGGL((stream_kernel<Cfg, false>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
+    hipLaunchKernelGGL((stream_kernel<Cfg, false, 0, EPI>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
   return DG_OK;
+}
+
+template <class Cfg, int LAY = 0>
+dg_status launch_stream(const Problem& p, int64_t blocks, hipStream_t stream) {
+  (void)blocks;
+  return launch_stream_as<Cfg, LAY, kEpiNone>(p, Epilogue{}, stream);
 }
 
 using Stream1x10 = StreamCfg<4, 1, 10>;
@@ -476,6 +499,7 @@ using Stream8w4 = StreamCfg<8, 1, 4>;
 using Stream2w4 = StreamCfg<2, 1, 4>;
 
 typedef dg_status (*Launcher)(const Problem&, int64_t, hipStream_t);
+typedef dg_status (*EpiLauncher)(const Problem&, const Epilogue&, hipStream_t);
 typedef bool (*Fits)(int64_t M, int64_t N, int64_t K);
 
 struct CfgEntry {
@@ -484,7 +508,19 @@ struct CfgEntry {
   int max_m;                            // skinny: rows it covers; 0 = any
   int max_kb;                           // K/128 it supports; 0 = any
   Fits fits;                            // further shape test (dense); NULL = none
+  EpiLauncher bias_act, bias_act_fp8;   // dense with the fused epilogues; NULL = none
 };
+
+template <class Cfg, int EPI>
+dg_status launch_pipe_epi(const Problem& p, const Epilogue& ep, hipStream_t stream) {
+  return launch_pipe_as<Cfg, kDense, 0, EPI>(p, 1, ep, stream);
+}
+
+template <int EPI>
+dg_status launch_pipe128_epi(const Problem& p, const Epilogue& ep, hipStream_t stream) {
+  return p.K / kKBlock >= kLongKB ? launch_pipe_epi<Pipe128x256L, EPI>(p, ep, stream)
+                                  : launch_pipe_epi<Pipe128x256, EPI>(p, ep, stream);
+}
 
 // The pipelined kernel addresses a tile's rows with 32-bit offsets below 256 * K
 // bytes; this bound keeps them under 2^31.
@@ -496,27 +532,33 @@ const CfgEntry kTable[] = {
     {"tile64x64_w2x2", launch_tile<Cfg64, kDense>, launch_tile<Cfg64, kContiguous>,
      launch_tile<Cfg64, kMasked>, 0, 0},
     {"pipe256x128", launch_pipe<Pipe256x128, kDense>, launch_pipe<Pipe256x128, kContiguous>,
-     launch_pipe<Pipe256x128, kMasked>, 0, kPipeMaxKB},
+     launch_pipe<Pipe256x128, kMasked>, 0, kPipeMaxKB, nullptr,
+     launch_pipe_epi<Pipe256x128, kEpiBf16>, launch_pipe_epi<Pipe256x128, kEpiFp8>},
     {"pipe128x256", launch_pipe128<kDense>, launch_pipe128<kContiguous>,
-     launch_pipe128<kMasked>, 0, kPipeMaxKB},
+     launch_pipe128<kMasked>, 0, kPipeMaxKB, nullptr, launch_pipe128_epi<kEpiBf16>,
+     launch_pipe128_epi<kEpiFp8>},
     {"skinny_w4_tn1_d3", launch_skinny<SkinnyCfg<4, 1, 3>>, nullptr, nullptr, 64, 0},
-    {"skinny_w4_tn1_d2", launch_skinny<SkinnyCfg<4, 1, 2>>, nullptr, nullptr, 64, 0},
+    {"skinny_w4_tn1_d2", launch_skinny<SkinnyCfg<4, 1, 2>>, nullptr, nullptr, 64, 0, nullptr,
+     launch_skinny_as<SkinnyCfg<4, 1, 2>, 0, kEpiBf16>},
     {"skinny_w4_tn1_d5", launch_skinny<SkinnyCfg<4, 1, 5>>, nullptr, nullptr, 64, 0},
-    {"skinny_w4_tn1_d8", launch_skinny<SkinnyCfg<4, 1, 8>>, nullptr, nullptr, 64, 0},
+    {"skinny_w4_tn1_d8", launch_skinny<SkinnyCfg<4, 1, 8>>, nullptr, nullptr, 64, 0, nullptr,
+     launch_skinny_as<SkinnyCfg<4, 1, 8>, 0, kEpiBf16>},
     {"skinny_w2_tn1_d3", launch_skinny<SkinnyCfg<2, 1, 3>>, nullptr, nullptr, 64, 0},
     {"skinny_w2_tn1_d5", launch_skinny<SkinnyCfg<2, 1, 5>>, nullptr, nullptr, 64, 0},
     {"skinny_w2_tn1_d8", launch_skinny<SkinnyCfg<2, 1, 8>>, nullptr, nullptr, 64, 0},
-    {"skinny_w8_tn1_d4", launch_skinny<SkinnyCfg<8, 1, 4>>, nullptr, nullptr, 64, 0},
-    {"skinny_w8_tn1_d2", launch_skinny<SkinnyCfg<8, 1, 2>>, nullptr, nullptr, 64, 0},
+    {"skinny_w8_tn1_d4", launch_skinny<SkinnyCfg<8, 1, 4>>, nullptr, nullptr, 64, 0, nullptr,
+     nullptr, launch_skinny_as<SkinnyCfg<8, 1, 4>, 0, kEpiFp8>},
+    {"skinny_w8_tn1_d2", launch_skinny<SkinnyCfg<8, 1, 2>>, nullptr, nullptr, 64, 0, nullptr,
+     nullptr, launch_skinny_as<SkinnyCfg<8, 1, 2>, 0, kEpiFp8>},
     {"skinny_w2_tn1_d2", launch_skinny<SkinnyCfg<2, 1, 2>>, nullptr, nullptr, 64, 0},
     {"stream_w4_tn1_d10", launch_stream<Stream1x10>, nullptr, nullptr, 64, 0,
-     stream_fits<Stream1x10>},
+     stream_fits<Stream1x10>, launch_stream_as<Stream1x10, 0, kEpiBf16>},
     {"stream_w4_tn2_d4", launch_stream<Stream2x4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream2x4>},
     {"stream_w4_tn1_d4", launch_stream<Stream1x4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream1x4>},
     {"stream_w8_tn1_d10", launch_stream<Stream8w10>, nullptr, nullptr, 64, 0,
-     stream_fits<Stream8w10>},
+     stream_fits<Stream8w10>, nullptr, launch_stream_as<Stream8w10, 0, kEpiFp8>},
     {"stream_w8_tn1_d4", launch_stream<Stream8w4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream8w4>},
     {"stream_w2_tn1_d4", launch_stream<Stream2w4>, nullptr, nullptr, 64, 0,
@@ -574,6 +616,35 @@ int select_config(int kind, int64_t m, int64_t M, int64_t n, int64_t k, int32_t 
   // (measured 128x256x512: 9.3 against 12.0 us; 128x1024x4096: 18.1 against 19.2 us)
   if (kind == kDense && M <= 128 && (n + 255) / 256 < 8) return find_cfg("pipe256x128");
   return find_cfg("pipe128x256");
+}
+
+// The same for the dense GEMM with a fused epilogue; -1 when K is beyond the kernels that
+// have one. bf16 output: select_config's choice. FP8 output: M <= 64 needs 128-column
+// workgroups, so that one workgroup holds whole 1x128 blocks of a row.
+int select_epi_config(bool fp8, int64_t M, int64_t N, int64_t K) {
+  const auto has = [&](int id) {
+    return (fp8 ? kTable[id].bias_act_fp8 : kTable[id].bias_act) && cfg_applies(id, kDense, M, N, K);
+  };
+  const char* forced = getenv("DG_FORCE_CONFIG");
+  if (forced && *forced) {
+    const int id = find_cfg(forced);
+    if (id >= 0 && has(id)) return id;
+  }
+  const int64_t KB = K / kKBlock;
+  if (M > 64) {
+    if (KB > kPipeMaxKB) return -1;
+    return find_cfg(M <= 128 && (N + 255) / 256 < 8 ? "pipe256x128" : "pipe128x256");
+  }
+  const int BN = fp8 ? 128 : 64;
+  const int s1 = find_cfg(fp8 ? "stream_w8_tn1_d10" : "stream_w4_tn1_d10");
+  if (KB >= 16 && has(s1)) return s1;
+  const int64_t tiles = (N + BN - 1) / BN;
+  int64_t s = kCUs / tiles;
+  s = s > 8 ? 8 : (s < 1 ? 1 : s);
+  if (s > KB) s = KB;
+  const bool deep = (KB + s - 1) / s >= 6;
+  return find_cfg(fp8 ? (deep ? "skinny_w8_tn1_d4" : "skinny_w8_tn1_d2")
+                      : (deep ? "skinny_w4_tn1_d8" : "skinny_w4_tn1_d2"));
 }
 
 bool print_configs() {
@@ -1040,6 +1111,232 @@ dg_status dg_describe_config(int32_t kind, int64_t M, int64_t N, int64_t K, int3
   const int id = select_config(kind, m, M, N, K, G);
   snprintf(buf, (size_t)len, "%s", kTable[id].name);
   return DG_OK;
+}
+
+}  // extern "C"
+
+namespace dg {
+namespace {
+
+// ---------------------------------------------------------------- GEMM with a fused epilogue
+
+bool known_dtype(int32_t t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
+bool known_act(int32_t a) { return a >= DG_ACT_NONE && a <= DG_ACT_GELU_TANH; }
+
+dg_status gemm_epilogue(const void* A, const void* B, const void* sfA, int32_t sfa_packed,
+                        const float* sfB, int64_t M, int64_t N, int64_t K, void* C, bool fp8,
+                        int32_t bias_dtype, const Epilogue& ep, void* stream) {
+  if (M < 0) return fail(DG_ERR_BAD_SHAPE, "negative M=%lld", (long long)M);
+  if (!known_act(ep.act)) return fail(DG_ERR_BAD_SHAPE, "activation=%d is unknown", ep.act);
+  if (ep.bias && !known_dtype(bias_dtype))
+    return fail(DG_ERR_BAD_SHAPE, "bias_dtype=%d is neither DG_DTYPE_F32 nor DG_DTYPE_BF16", bias_dtype);
+  void* out = fp8 ? (void*)ep.codes : C;
+  dg_status s = check_common(A, B, out, sfA, sfB, N, K, M > 0 && N > 0);
+  if (s != DG_OK) return s;
+  if (fp8 && N % 128 != 0) return fail(DG_ERR_BAD_SHAPE, "N=%lld is not a multiple of 128", (long long)N);
+  if (M == 0 || N == 0) return DG_OK;
+  if (fp8 && !ep.so.sf) return fail(DG_ERR_NULL_POINTER, "NULL sf");
+  if (fp8 && !aligned(ep.so.sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
+  if (!aligned(ep.bias, 16) || !aligned(ep.residual, 16) || !aligned(ep.pre, 16))
+    return fail(DG_ERR_MISALIGNED, "bias, residual and pre must be 16-byte aligned");
+  if (M > (int64_t)1 << 30) return fail(DG_ERR_UNSUPPORTED_SHAPE, "M beyond 2^30");
+  const int id = select_epi_config(fp8, M, N, K);
+  if (id < 0)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "K=%lld with M > 64: the fused epilogues go up to K = %lld",
+                (long long)K, (long long)kPipeMaxKB * kKBlock);
+  maybe_print(kDense, M, N, K, 1, id, fp8 ? " (fused epilogue, FP8 output)" : " (fused epilogue)");
+  Problem p{};
+  p.A = (const uint8_t*)A;
+  p.B = (const uint8_t*)B;
+  p.C = (uint16_t*)C;
+  p.sfA = (const uint8_t*)sfA;
+  p.sfa_packed = sfa_packed != 0;
+  p.sfB = sfB;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.G = 1;
+  return (fp8 ? kTable[id].bias_act_fp8 : kTable[id].bias_act)(p, ep, (hipStream_t)stream);
+}
+
+// ---------------------------------------------------------------- norm and its backward
+
+// Threads of a row's workgroup: 16 values each, in one chunk or (K > 16384) two.
+int norm_chunks(int64_t K) { return K > 16 * kNormMaxThreads ? 2 : 1; }
+unsigned norm_threads(int64_t K) {
+  const int64_t t = (K / 16 + norm_chunks(K) - 1) / norm_chunks(K);
+  return (unsigned)((t + 63) / 64 * 64);
+}
+
+// Row r goes to workgroup r mod G: as many workgroups as the CUs hold at once (2048 threads
+// each), at most one per row.
+int64_t norm_grid(int64_t M, unsigned threads) {
+  const int64_t g = kCUs * (2048 / threads);
+  return M < g ? M : g;
+}
+
+dg_status check_rows(int64_t M, int64_t K, const char* k) {
+  if (M < 0 || K < 0)
+    return fail(DG_ERR_BAD_SHAPE, "negative size (M=%lld, %s=%lld)", (long long)M, k, (long long)K);
+  if (K % kKBlock != 0) return fail(DG_ERR_BAD_SHAPE, "%s=%lld is not a multiple of 128", k, (long long)K);
+  if (K > 0 && M > ((int64_t)1 << 40) / K) return fail(DG_ERR_UNSUPPORTED_SHAPE, "M*%s beyond 2^40", k);
+  return DG_OK;
+}
+
+dg_status check_norm(int32_t x_dtype, int32_t w_dtype, int64_t M, int64_t K) {
+  if (!known_dtype(x_dtype) || !known_dtype(w_dtype))
+    return fail(DG_ERR_BAD_SHAPE, "x_dtype=%d, w_dtype=%d: neither DG_DTYPE_F32 nor DG_DTYPE_BF16",
+                x_dtype, w_dtype);
+  const dg_status s = check_rows(M, K, "K");
+  if (s != DG_OK) return s;
+  if (K > kNormMaxK) return fail(DG_ERR_UNSUPPORTED_SHAPE, "K=%lld beyond %d", (long long)K, kNormMaxK);
+  return DG_OK;
+}
+
+dg_status launched(const char* what) {
+  const hipError_t err = hipGetLastError();
+  return err == hipSuccess ? DG_OK : fail(DG_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(err));
+}
+
+// out[n] = sum over R rows of part[R][N] (N % 16 == 0); R = 0 writes zeros
+dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N, hipStream_t st) {
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)(N / 16)), dim3(256), 0, st, part, out, (int)R,
+                     (int)N);
+  return launched("column_sum_kernel");
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+dg_status dg_fp8_gemm_nt_bias_act(const void* A, const void* B, void* C, const void* sfA,
+                                  int32_t sfA_packed, const float* sfB, const void* bias,
+                                  int32_t bias_dtype, int32_t activation, const void* residual,
+                                  void* pre, int64_t M, int64_t N, int64_t K, void* stream) {
+  g_detail[0] = 0;
+  Epilogue ep{};
+  ep.bias = bias;
+  ep.bias_bf16 = bias_dtype == DG_DTYPE_BF16;
+  ep.act = activation;
+  ep.residual = (const uint16_t*)residual;
+  ep.pre = (uint16_t*)pre;
+  return gemm_epilogue(A, B, sfA, sfA_packed, sfB, M, N, K, C, false, bias_dtype, ep, stream);
+}
+
+dg_status dg_fp8_gemm_nt_bias_act_fp8(const void* A, const void* B, void* codes, void* sf,
+                                      int32_t sf_packed, const void* sfA, int32_t sfA_packed,
+                                      const float* sfB, const void* bias, int32_t bias_dtype,
+                                      int32_t activation, void* pre, int64_t M, int64_t N,
+                                      int64_t K, void* stream) {
+  g_detail[0] = 0;
+  Epilogue ep{};
+  ep.bias = bias;
+  ep.bias_bf16 = bias_dtype == DG_DTYPE_BF16;
+  ep.act = activation;
+  ep.pre = (uint16_t*)pre;
+  ep.codes = (uint8_t*)codes;
+  ep.so = ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)};
+  return gemm_epilogue(A, B, sfA, sfA_packed, sfB, M, N, K, nullptr, true, bias_dtype, ep, stream);
+}
+
+dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dtype,
+                               const void* weight, int32_t w_dtype, float eps, void* h, float* rstd,
+                               void* codes, void* sf, int32_t sf_packed, int64_t M, int64_t K,
+                               void* stream) {
+  g_detail[0] = 0;
+  const dg_status s = check_norm(x_dtype, w_dtype, M, K);
+  if (s != DG_OK) return s;
+  if (!(eps > 0.f && eps < INFINITY)) return fail(DG_ERR_BAD_SHAPE, "eps=%g is not positive", (double)eps);
+  if (M == 0 || K == 0) return DG_OK;
+  if (!x || !weight || !codes || !sf) return fail(DG_ERR_NULL_POINTER, "NULL x, weight, codes or sf");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(codes, 16))
+    return fail(DG_ERR_MISALIGNED, "x, residual, weight, h and codes must be 16-byte aligned");
+  if (!aligned(rstd, 4) || !aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "rstd and sf must be 4-byte aligned");
+  NormArgs a{x, residual, weight, h, rstd, (uint8_t*)codes,
+             ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(K / 128)}, M, (int32_t)K, eps,
+             w_dtype == DG_DTYPE_BF16};
+  const unsigned nt = norm_threads(K);
+  const dim3 grid((unsigned)norm_grid(M, nt)), block(nt);
+  const hipStream_t st = (hipStream_t)stream;
+  const bool two = norm_chunks(K) == 2;
+  if (x_dtype == DG_DTYPE_BF16) {
+    if (two) hipLaunchKernelGGL((rmsnorm_kernel<true, 2>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((rmsnorm_kernel<true, 1>), grid, block, 0, st, a);
+  } else {
+    if (two) hipLaunchKernelGGL((rmsnorm_kernel<false, 2>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((rmsnorm_kernel<false, 1>), grid, block, 0, st, a);
+  }
+  return launched("rmsnorm_kernel");
+}
+
+dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
+                              const void* weight, int32_t w_dtype, const float* rstd, void* dx,
+                              float* dweight, int64_t M, int64_t K, void* stream) {
+  g_detail[0] = 0;
+  dg_status s = check_norm(x_dtype, w_dtype, M, K);
+  if (s != DG_OK || K == 0) return s;
+  if (!dweight || (M > 0 && (!dy || !h || !weight || !rstd || !dx)))
+    return fail(DG_ERR_NULL_POINTER, "NULL dy, h, weight, rstd, dx or dweight");
+  if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(weight, 16) ||
+      !aligned(dx, 16) || !aligned(dweight, 16))
+    return fail(DG_ERR_MISALIGNED, "dy, dh, h, weight, dx and dweight must be 16-byte aligned");
+  if (!aligned(rstd, 4)) return fail(DG_ERR_MISALIGNED, "rstd must be 4-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  if (M == 0) return launch_column_sum(nullptr, dweight, 0, K, st);
+  const unsigned nt = norm_threads(K);
+  const int64_t G = norm_grid(M, nt);
+  float* part = nullptr;
+  uint32_t* counters = nullptr;
+  s = get_workspace(st, (size_t)(G * K) * sizeof(float), 0, &part, &counters);
+  if (s != DG_OK) return s;
+  NormBwdArgs a{dy, dh, h, weight, rstd, dx, part, M, (int32_t)K, w_dtype == DG_DTYPE_BF16};
+  const dim3 grid((unsigned)G), block(nt);
+  const bool two = norm_chunks(K) == 2;
+  if (x_dtype == DG_DTYPE_BF16) {
+    if (two) hipLaunchKernelGGL((rmsnorm_backward_kernel<true, 2>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((rmsnorm_backward_kernel<true, 1>), grid, block, 0, st, a);
+  } else {
+    if (two) hipLaunchKernelGGL((rmsnorm_backward_kernel<false, 2>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((rmsnorm_backward_kernel<false, 1>), grid, block, 0, st, a);
+  }
+  s = launched("rmsnorm_backward_kernel");
+  return s == DG_OK ? launch_column_sum(part, dweight, G, K, st) : s;
+}
+
+dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t activation, void* codes,
+                                   void* sf, int32_t sf_packed, float* dbias, int64_t M, int64_t N,
+                                   void* stream) {
+  g_detail[0] = 0;
+  if (!known_act(activation)) return fail(DG_ERR_BAD_SHAPE, "activation=%d is unknown", activation);
+  dg_status s = check_rows(M, N, "N");
+  if (s != DG_OK || N == 0) return s;
+  if (N > (int64_t)1 << 30) return fail(DG_ERR_UNSUPPORTED_SHAPE, "N beyond 2^30");
+  if (M > 0 && (!dc || !codes || !sf || (!pre && activation != DG_ACT_NONE)))
+    return fail(DG_ERR_NULL_POINTER, "NULL dc, pre, codes or sf");
+  if (!aligned(dc, 16) || !aligned(pre, 16) || !aligned(codes, 16) || !aligned(dbias, 16))
+    return fail(DG_ERR_MISALIGNED, "dc, pre, codes and dbias must be 16-byte aligned");
+  if (!aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, N, st) : DG_OK;
+  const int64_t strips = (N + 1023) / 1024;
+  // row groups: about eight workgroups per CU, at least 4 rows (one per wave) each
+  int64_t groups = (8 * kCUs + strips - 1) / strips;
+  if (groups > (M + 3) / 4) groups = (M + 3) / 4;
+  int64_t rows = ((M + groups - 1) / groups + 3) / 4 * 4;
+  groups = (M + rows - 1) / rows;
+  float* part = nullptr;
+  uint32_t* counters = nullptr;
+  if (dbias) {
+    s = get_workspace(st, (size_t)(groups * N) * sizeof(float), 0, &part, &counters);
+    if (s != DG_OK) return s;
+  }
+  ActBwdArgs a{(const uint16_t*)dc, (const uint16_t*)pre, (uint8_t*)codes,
+               ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)}, part, M, rows,
+               (int32_t)N, activation, (int32_t)strips};
+  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)(strips * groups)), dim3(256), 0, st, a);
+  s = launched("act_backward_kernel");
+  return s == DG_OK && dbias ? launch_column_sum(part, dbias, groups, N, st) : s;
 }
 
 }  // extern "C"

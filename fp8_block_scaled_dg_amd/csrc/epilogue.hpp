@@ -1,0 +1,122 @@
+// epilogue.hpp -- what the dense GEMM can do to an fp32 output value before its one rounding:
+//
+//   z = acc + bias[n];  pre[m][n] = bf16(z) (optional)
+//   kEpiBf16: C[m][n] = bf16(act(z) + residual[m][n])
+//   kEpiFp8:  codes and scales of act(z), quantized per 1x128 block (quant_kernel.hpp)
+//
+// The GEMM kernels pass their fp32 tile through LDS and hand each lane eight consecutive
+// columns of one row at a time, so that the bias is read once per lane and the residual,
+// pre and C move in 16-byte pieces of whole row segments.
+#pragma once
+
+#include "gemm_kernel.hpp"
+#include "norm_kernel.hpp"
+
+namespace dg {
+
+enum Epi : int { kEpiNone = 0, kEpiBf16 = 1, kEpiFp8 = 2 };
+
+struct Epilogue {
+  const void* bias;          // [N] bf16 or fp32; NULL: none
+  const uint16_t* residual;  // [M][N] bf16; NULL: none (may be C itself)
+  uint16_t* pre;             // [M][N] bf16; NULL: not stored
+  uint8_t* codes;            // kEpiFp8: e4m3fn [M][N]
+  ScaleOut so;               // kEpiFp8: scales, so.KB = N / 128
+  int32_t bias_bf16;
+  int32_t act;
+};
+
+// bias of columns col .. col + 7 (zero without one)
+__device__ __forceinline__ void epi_bias8(const Epilogue& ep, int64_t col, float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  if (!ep.bias) return;
+  if (ep.bias_bf16) {
+    const v4u u = *(const v4u*)((const uint16_t*)ep.bias + col);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      b[2 * j] = __uint_as_float(u[j] << 16);
+      b[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+    }
+  } else {
+    const v4f* p = (const v4f*)((const float*)ep.bias + col);
+    const v4f x = p[0], y = p[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = x[j], b[4 + j] = y[j];
+  }
+}
+
+__device__ __forceinline__ v4u epi_pack8(const float (&v)[8]) {
+  return v4u{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+             pack_bf16(v[6], v[7])};
+}
+
+// v (products at row, col .. col + 7, element offset off = row * N + col) -> act(v + b),
+// storing pre on the way
+__device__ __forceinline__ void epi_act8(const Epilogue& ep, const float (&b)[8], int64_t off,
+                                         float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
+  if (ep.pre) __builtin_nontemporal_store(epi_pack8(v), (v4u*)(ep.pre + off));
+  act_apply(v, ep.act);
+}
+
+// + residual, one rounding, store
+__device__ __forceinline__ void epi_store8(v4u res, uint16_t* C, int64_t off, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] += __uint_as_float(res[j] << 16);
+    v[2 * j + 1] += __uint_as_float(res[j] & 0xFFFF0000u);
+  }
+  __builtin_nontemporal_store(epi_pack8(v), (v4u*)(C + off));
+}
+
+// Row pitch, in floats, of the fp32 tile that the M <= 64 kernels leave in LDS: 4 floats
+// past BN spread the rows over the banks.
+template <int BN>
+constexpr int kEpiPitch = BN + 4;
+
+// Finishes the fp32 tile out[64][kEpiPitch<BN>] of columns n0 .. n0 + BN - 1 (all threads of
+// the workgroup, after a barrier): 8 columns of a row per thread and step. kEpiFp8: BN = 128,
+// 16 neighbouring lanes hold a row's 1x128 block.
+template <int BN, int NT, int EPI>
+__device__ __forceinline__ void epi_finish_tile(const Problem& p, int64_t n0, const float* out,
+                                                const Epilogue& ep) {
+  static_assert(EPI != kEpiFp8 || BN == 128, "a scale block per tile row");
+  constexpr int LPR = BN / 8;  // lanes per row
+  static_assert(64 % LPR == 0 && (64 * LPR) % NT == 0, "whole rows per wave");
+  const int64_t N = p.N;
+#pragma unroll 1
+  for (int c = threadIdx.x; c < 64 * LPR; c += NT) {
+    const int row = c / LPR, col0 = (c % LPR) * 8;
+    const int64_t col = n0 + col0, off = row * N + col;
+    if (row >= p.M || col >= N) continue;
+    v4u res = {0, 0, 0, 0};
+    if (EPI == kEpiBf16 && ep.residual)
+      res = __builtin_nontemporal_load((const v4u*)(ep.residual + off));
+    float b[8], x[8];
+    epi_bias8(ep, col, b);
+    const v4f lo = *(const v4f*)(out + row * kEpiPitch<BN> + col0);
+    const v4f hi = *(const v4f*)(out + row * kEpiPitch<BN> + col0 + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
+    epi_act8(ep, b, off, x);
+    if (EPI == kEpiBf16) {
+      epi_store8(res, p.C, off, x);
+    } else {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 16));
+      const int e = scale_exp(ep.so, m);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], -e);
+      *(uint2*)(ep.codes + off) =
+          make_uint2(quant_e4m3fn_x4(x[0], x[1], x[2], x[3]), quant_e4m3fn_x4(x[4], x[5], x[6], x[7]));
+      if (col0 == 0) store_scale(ep.so, row, (int)(col >> 7), e);
+    }
+  }
+}
+
+}  // namespace dg

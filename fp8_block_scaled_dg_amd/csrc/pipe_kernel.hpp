@@ -37,6 +37,7 @@
 // epilogue stores only produced rows and in-range columns.
 #pragma once
 
+#include "epilogue.hpp"
 #include "gemm_kernel.hpp"
 #include "quant_kernel.hpp"
 
@@ -768,6 +769,114 @@ __device__ __forceinline__ void pipe_store(const Problem& p, const TileView& v, 
   }
 }
 
+// The dense tile's epilogue with bias, activation and residual (EPI = kEpiBf16) or with
+// bias, activation and quantization (kEpiFp8). A wave passes its fp32 64x64 sub-tile
+// through its 4 KB of LDS stage 2, 16 rows at a time (256 bytes a row, 16-byte chunk q of
+// row r at q ^ r), and reads it back with 8 lanes per row, 8 columns each: a lane's columns
+// are the same in all rows, so it loads its bias once, and residual, pre and C move as whole
+// 128-byte row segments. The residual of a 16-row pass is loaded before the pass's LDS
+// traffic. The activation sits in a loop that is not unrolled: it costs code for 8 values,
+// not for 64.
+// kEpiFp8: a row's 1x128 block is shared by two waves (wn and wn ^ 1), which hold its two
+// 64-column halves. Each keeps its 64 values per lane, the row maxima meet in pipe_rmax
+// behind one barrier, and the codes go out as 8 bytes per lane, 64-byte row segments. No
+// second barrier is needed: the next tile's maxima are written behind its main loop's.
+__shared__ float pipe_rmax[8][64];
+
+template <class Cfg, int EPI>
+__device__ __forceinline__ void pipe_store_epi(const Problem& p, const TileView& v,
+                                               const v16f (&acc)[Cfg::TM][Cfg::TN],
+                                               const Epilogue& ep) {
+  static_assert(Cfg::TM == 2 && Cfg::TN == 2 && Cfg::NW * 4096 <= kPipeStageBytes,
+                "64x64 sub-tiles, 4 KB per wave");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t N = p.N;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  const int r32 = lane & 31, g = lane >> 5;
+  uint8_t* lds = pipe_stage2 + wave * 4096;
+  const int rr = lane >> 3, ch = lane & 7;  // read side: rows rr + 8k, columns 8 ch ..
+  const int64_t col = v.n0 + wn * 64 + 8 * ch, row0 = v.m0 + wm * 64 + rr;
+  const bool col_ok = col < N;
+  float b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  if (col_ok) epi_bias8(ep, col, b);
+  float keep[EPI == kEpiFp8 ? 8 : 1][8];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {  // 16-row passes
+    v4u res[2] = {v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}};
+    if (EPI == kEpiBf16 && ep.residual) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t row = row0 + 16 * h + 8 * k;
+        if (col_ok && row < p.M)
+          res[k] = __builtin_nontemporal_load((const v4u*)(ep.residual + row * N + col));
+      }
+    }
+    if ((r32 >> 4) == (h & 1)) {
+      const int r = r32 & 15;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const v16f& t = acc[h >> 1][j];
+          *(v4f*)(lds + r * 256 + (((8 * j + 2 * e4 + g) ^ r) << 4)) =
+              v4f{t[4 * e4], t[4 * e4 + 1], t[4 * e4 + 2], t[4 * e4 + 3]};
+        }
+    }
+    // the wave's LDS accesses run in order; the fences keep the compiler from moving
+    // the reads of other lanes' data above the writes, and the next writes above them
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    wait_vm_lgkm0<63>();
+    float x[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 8 * k + rr;
+      const v4f lo = *(const v4f*)(lds + r * 256 + (((2 * ch) ^ r) << 4));
+      const v4f hi = *(const v4f*)(lds + r * 256 + (((2 * ch + 1) ^ r) << 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[k][i] = lo[i], x[k][4 + i] = hi[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t row = row0 + 16 * h + 8 * k;
+      const bool ok = col_ok && row < p.M;
+      const int64_t off = row * N + col;
+      if (ok) epi_act8(ep, b, off, x[k]);
+      if (EPI == kEpiBf16) {
+        if (ok) epi_store8(res[k], v.C, off, x[k]);
+      } else {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          keep[2 * h + k][i] = x[k][i];
+          m = fmaxf(m, fabsf(x[k][i]));
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 8));
+        if (ch == 0) pipe_rmax[wave][16 * h + 8 * k + rr] = m;
+      }
+    }
+  }
+  if (EPI == kEpiFp8) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t row = row0 + 8 * k;
+      const int e = scale_exp(ep.so, fmaxf(pipe_rmax[wave][8 * k + rr], pipe_rmax[wave ^ 1][8 * k + rr]));
+      if (!col_ok || row >= p.M) continue;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = ldexpf(keep[k][i], -e);
+      *(uint2*)(ep.codes + row * N + col) =
+          make_uint2(quant_e4m3fn_x4(y[0], y[1], y[2], y[3]), quant_e4m3fn_x4(y[4], y[5], y[6], y[7]));
+      if ((wn & 1) == 0 && ch == 0) store_scale(ep.so, row, (int)(col >> 7), e);
+    }
+  }
+}
+
 // Where the fused SwiGLU epilogue writes: e4m3fn codes [rows][I] and fp32 scales
 // [rows][I/128] of h = silu(gate) * up (rows as in the GEMM's A).
 struct SwigluOut {
@@ -866,17 +975,21 @@ __device__ __forceinline__ void pipe_store_swiglu(const Problem& p, const TileVi
   __syncthreads();  // the LDS is free again (the contiguous layout may run another pass)
 }
 
-template <class Cfg, int KIND, bool SWIGLU = false, int LAY = 0>
+template <class Cfg, int KIND, bool SWIGLU = false, int LAY = 0, int EPI = kEpiNone>
 __device__ __forceinline__ void pipe_tile(const Problem& p, const TileView& v, int expert,
                                           int valid_rows, uint32_t quarters = ~0u,
-                                          SwigluOut sw = SwigluOut{}) {
+                                          SwigluOut sw = SwigluOut{},
+                                          const Epilogue& ep = Epilogue{}) {
   v16f acc[Cfg::TM][Cfg::TN];
   if constexpr (SWIGLU) {
     pipe_mainloop<Cfg>(p, v, 0, (int)(p.K / kKBlock), acc, quarters, sw.I - 128);
     pipe_store_swiglu<Cfg, KIND>(p, v, expert, valid_rows, acc, sw);
   } else {
     pipe_mainloop<Cfg, LAY>(p, v, 0, (int)(p.K / kKBlock), acc, quarters);
-    pipe_store<Cfg, KIND>(p, v, expert, valid_rows, acc);
+    if constexpr (EPI != kEpiNone)
+      pipe_store_epi<Cfg, EPI>(p, v, acc, ep);
+    else
+      pipe_store<Cfg, KIND>(p, v, expert, valid_rows, acc);
   }
 }
 
@@ -944,13 +1057,14 @@ struct PipeArgs {
   int32_t parts;       // dense: K parts of each remaining tile
   int32_t items;       // work items: dense full tiles + split parts, or the grid's tiles
   SwigluOut sw;        // fused SwiGLU epilogue (grouped layouts): outputs and I
+  Epilogue ep;         // dense: bias, activation, residual or quantization (EPI kernels)
 };
 
 // Dense tail tile: K-blocks [kb_lo, kb_hi) of tile `tt` (index among the split
 // tiles), part `part` of `parts`. Each part writes its fp32 tile with device-scope
 // stores and counts its arrival; the last part to arrive adds the parts in part
 // order -- a fixed order, so the result is deterministic -- and stores bf16.
-template <class Cfg, int LAY>
+template <class Cfg, int LAY, int EPI>
 __device__ __forceinline__ void pipe_split_tile(const PipeArgs& a, const TileView& v, int tt,
                                                 int part, int kb_lo, int kb_hi) {
   constexpr int TM = Cfg::TM, TN = Cfg::TN, BMN = Cfg::BM * Cfg::BN;
@@ -1010,7 +1124,10 @@ __device__ __forceinline__ void pipe_split_tile(const PipeArgs& a, const TileVie
   }
   if (tid == 0)
     __hip_atomic_store(&a.counters[tt], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  pipe_store<Cfg, kDense>(a.p, v, 0, (int)a.p.M, sum);
+  if constexpr (EPI != kEpiNone)
+    pipe_store_epi<Cfg, EPI>(a.p, v, sum, a.ep);
+  else
+    pipe_store<Cfg, kDense>(a.p, v, 0, (int)a.p.M, sum);
 }
 
 // One work item: a tile (or, dense, a K part of a tail tile). `item` plays the role
@@ -1018,9 +1135,10 @@ __device__ __forceinline__ void pipe_split_tile(const PipeArgs& a, const TileVie
 // SWIGLU (grouped layouts, 128x256 tiles): B is [gate; up] with 2 * sw.I rows per
 // expert, tile tn covers gate columns 128 tn.. and the matching up columns, and the
 // fused epilogue writes quantized h instead of bf16 C.
-template <class Cfg, int KIND, bool SWIGLU, int LAY>
+template <class Cfg, int KIND, bool SWIGLU, int LAY, int EPI>
 __device__ __forceinline__ void pipe_item(const PipeArgs& args, int item) {
   static_assert(LAY == 0 || (KIND == kDense && !SWIGLU), "other layouts: dense GEMM only");
+  static_assert(EPI == kEpiNone || KIND == kDense, "bias and activation: dense GEMM only");
   static_assert(!SWIGLU || KIND != kDense, "the fused epilogue is for the grouped layouts");
   constexpr int NSTEP = SWIGLU ? 128 : Cfg::BN;  // columns between consecutive N-tiles
   const Problem& p = args.p;
@@ -1039,7 +1157,7 @@ __device__ __forceinline__ void pipe_item(const PipeArgs& args, int item) {
     v.rows = p.M;
     v.B = p.B;
     v.sfB = p.sfB;
-    pipe_split_tile<Cfg, LAY>(args, v, tt, part, part * KB / args.parts,
+    pipe_split_tile<Cfg, LAY, EPI>(args, v, tt, part, part * KB / args.parts,
                               (part + 1) * KB / args.parts);
     return;
   }
@@ -1079,7 +1197,7 @@ __device__ __forceinline__ void pipe_item(const PipeArgs& args, int item) {
   if (KIND == kDense) {
     v.B = p.B;
     v.sfB = p.sfB;
-    pipe_tile<Cfg, KIND, false, LAY>(p, v, 0, (int)p.M);
+    pipe_tile<Cfg, KIND, false, LAY, EPI>(p, v, 0, (int)p.M, ~0u, SwigluOut{}, args.ep);
     return;
   }
   // contiguous: one pass per distinct expert id among the tile's rows, in
@@ -1119,10 +1237,10 @@ __device__ __forceinline__ void pipe_item(const PipeArgs& args, int item) {
 // blockIdx.x + gridDim.x, ... (gridDim.x is the item count, or a multiple of 8 when
 // smaller, so item i stays on XCD i % 8). A tile's stores drain while the next
 // tile's first DMAs are in flight, and no workgroup is dispatched per tile.
-template <class Cfg, int KIND, bool SWIGLU = false, int LAY = 0>
+template <class Cfg, int KIND, bool SWIGLU = false, int LAY = 0, int EPI = kEpiNone>
 __global__ void __launch_bounds__(Cfg::NT) pipe_kernel(PipeArgs args) {
   for (int item = blockIdx.x; item < args.items; item += gridDim.x)
-    pipe_item<Cfg, KIND, SWIGLU, LAY>(args, item);
+    pipe_item<Cfg, KIND, SWIGLU, LAY, EPI>(args, item);
 }
 
 }  // namespace dg

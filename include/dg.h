@@ -27,7 +27,8 @@
  *      - fp32 partial tiles and arrival counters, for calls that split K across
  *        workgroups (the M <= 64 kernels, and the last partial round of tiles of a
  *        larger dense GEMM);
- *      - transposed operand copies, for the NN / TN / TT calls.
+ *      - transposed operand copies, for the NN / TN / TT calls;
+ *      - fp32 partial column sums (in the partial tiles' buffer), for the backward calls.
  *    Calls on one stream share them in stream order; calls on different streams
  *    never share them. The buffers only grow. An outgrown buffer is retired, not
  *    freed: it stays allocated until dg_release_workspaces() or the end of the
@@ -74,7 +75,8 @@ typedef enum dg_status {
   DG_OK = 0,
   DG_ERR_NULL_POINTER = 1,      /* a required pointer is NULL                    */
   DG_ERR_BAD_SHAPE = 2,         /* negative size, K % 128 != 0, N % 16 != 0, G<1, */
-                                /* or an unknown dg_dtype                         */
+                                /* an unknown dg_dtype or dg_activation, or an    */
+                                /* eps that is not positive and finite            */
   DG_ERR_UNSUPPORTED_SHAPE = 3, /* valid but beyond what the kernels index       */
   DG_ERR_MISALIGNED = 4,        /* A/B/C not 16-byte or scales not 4-byte aligned */
   DG_ERR_NO_DEVICE = 5,         /* no usable gfx950 device                       */
@@ -259,6 +261,106 @@ typedef enum dg_dtype { DG_DTYPE_F32 = 0, DG_DTYPE_BF16 = 1 } dg_dtype;
 
 dg_status dg_quantize_fp8_1x128(const void* x, int32_t x_dtype, void* codes, float* sf,
                                 int64_t M, int64_t K, void* hip_stream);
+
+/*
+ * RMS norm with the residual's addition and an FP8 output: the layer input of a
+ * transformer block straight into the A operand and sfA of the GEMM calls above.
+ *   x, residual  [M][K], fp32 or bf16 (x_dtype); residual may be NULL (no addition)
+ *   weight       [K], fp32 or bf16 (w_dtype)
+ *   s = x + residual (in fp32, not rounded);  rstd[m] = 1 / sqrt(mean_k s^2 + eps)
+ *   y = s * rstd * weight;  codes, sf = y quantized as dg_quantize_fp8_1x128 quantizes
+ * Outputs:
+ *   h      [M][K] of x's type: s, rounded once (NULL: not stored; x or residual itself
+ *          may be passed, any other overlap may not)
+ *   rstd   fp32 [M] (NULL: not stored), for dg_rmsnorm_backward
+ *   codes  e4m3fn [M][K];  sf  fp32 [M][K/128], or with sf_packed != 0 the packed UE8M0
+ *          words uint32 [M][ceil(K/512)] of the *_ue8m0 calls, padding bytes zero,
+ *          exponents held at -127 or more
+ * Squares are summed in fp32. A row of zeros gives zero codes and scales 1. A row that
+ * holds a NaN, or an infinity, or whose squares overflow fp32, gives what the formula
+ * gives in fp32 (NaN codes 0x7F / 0xFF where y is NaN); the scales of a block that
+ * holds a NaN are unspecified.
+ * K % 128 == 0, K <= 32768; eps positive and finite; M * K <= 2^40; x, residual, weight,
+ * h and codes 16-byte aligned, rstd and sf 4-byte aligned. M == 0 or K == 0 returns DG_OK
+ * and launches nothing.
+ */
+dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dtype,
+                               const void* weight, int32_t w_dtype, float eps, void* h,
+                               float* rstd, void* codes, void* sf, int32_t sf_packed, int64_t M,
+                               int64_t K, void* hip_stream);
+
+/*
+ * Backward of the norm (the quantization taken as the identity): with xh = h * rstd and
+ * g = weight * dy,
+ *   dx      [M][K] = rstd * (g - xh * mean_k(g * xh)) + dh
+ *   dweight fp32 [K] = sum_m dy * xh
+ * dy, dh, h and dx have type x_dtype; dh (NULL: zero) is the gradient that reaches h
+ * along the residual stream, and dx is the gradient of x and of the residual. dx may be
+ * dy, dh or h itself. Column sums are added in a fixed order (bitwise deterministic for a
+ * given shape). Limits, alignment (dweight 16 bytes) and errors as above; M == 0 writes
+ * zeros to dweight.
+ */
+dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
+                              const void* weight, int32_t w_dtype, const float* rstd, void* dx,
+                              float* dweight, int64_t M, int64_t K, void* hip_stream);
+
+/*
+ * Activations of the fused epilogues (fp32): max(x, 0); x / (1 + e^-x); x * Phi(x) with
+ * Phi the normal distribution function (the "erf" form); x * (1 + tanh u) / 2 with
+ * u = sqrt(2/pi) * (x + 0.044715 x^3).
+ */
+typedef enum dg_activation {
+  DG_ACT_NONE = 0,
+  DG_ACT_RELU = 1,
+  DG_ACT_SILU = 2,
+  DG_ACT_GELU = 3,
+  DG_ACT_GELU_TANH = 4
+} dg_activation;
+
+/*
+ * Dense NT GEMM with bias, activation and residual in its epilogue. With z = the block-
+ * scaled product of dg_fp8_gemm_nt in fp32, before rounding, plus bias[n]:
+ *   C[m][n] = bf16( activation(z) + residual[m][n] )      pre[m][n] = bf16( z )
+ *   bias      [N] fp32 or bf16 (bias_dtype); NULL: none
+ *   residual  bf16 [M][N]; NULL: none; may be C itself, any other overlap may not
+ *   pre       bf16 [M][N], for the backward of the activation; NULL: not stored
+ *   sfA       fp32 [M][K/128], or with sfA_packed != 0 packed UE8M0 words
+ * Every value is rounded once. Shapes, alignment (bias, residual and pre 16 bytes), stream,
+ * workspace and error rules of dg_fp8_gemm_nt; with M > 64, K <= 2^22.
+ */
+dg_status dg_fp8_gemm_nt_bias_act(const void* A, const void* B, void* C, const void* sfA,
+                                  int32_t sfA_packed, const float* sfB, const void* bias,
+                                  int32_t bias_dtype, int32_t activation, const void* residual,
+                                  void* pre, int64_t M, int64_t N, int64_t K, void* hip_stream);
+
+/*
+ * The same product with an FP8 output: activation(z) quantized as dg_quantize_fp8_1x128
+ * quantizes, without a bf16 copy in between, so that it is the next GEMM's A and sfA.
+ *   codes  e4m3fn [M][N];  sf  fp32 [M][N/128] or (sf_packed) uint32 [M][ceil(N/512)] as
+ *          in dg_rmsnorm_fp8_1x128
+ * N % 128 == 0; codes and pre 16-byte aligned, sf 4-byte aligned. Codes and scales of a
+ * block holding an infinity or NaN are unspecified.
+ */
+dg_status dg_fp8_gemm_nt_bias_act_fp8(const void* A, const void* B, void* codes, void* sf,
+                                      int32_t sf_packed, const void* sfA, int32_t sfA_packed,
+                                      const float* sfB, const void* bias, int32_t bias_dtype,
+                                      int32_t activation, void* pre, int64_t M, int64_t N,
+                                      int64_t K, void* hip_stream);
+
+/*
+ * Backward of the epilogue: with p = dc * activation'(pre),
+ *   codes, sf = p quantized as dg_quantize_fp8_1x128 quantizes: the A operand and sfA of
+ *     dg_fp8_gemm_nn(codes, B, dA, sf, sfB^T) with B [N][K] as it is stored for the forward
+ *     call, which gives dA [M][K]
+ *   dbias  fp32 [N] = sum_m p (before quantization; NULL: not computed)
+ *   dc, pre  bf16 [M][N] (pre may be NULL with DG_ACT_NONE). relu'(0) = 0.
+ * N % 128 == 0; M * N <= 2^40; dc, pre, codes and dbias 16-byte aligned, sf 4-byte aligned.
+ * Column sums are added in a fixed order. M == 0 writes zeros to dbias. Codes and scales of
+ * a block holding an infinity or NaN are unspecified.
+ */
+dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t activation,
+                                   void* codes, void* sf, int32_t sf_packed, float* dbias,
+                                   int64_t M, int64_t N, void* hip_stream);
 
 /*
  * Frees every library-owned buffer (split-K partials and counters, transposed operand
