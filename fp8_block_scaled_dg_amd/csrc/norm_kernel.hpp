@@ -31,48 +31,99 @@ typedef float nk_v2f __attribute__((ext_vector_type(2)));
 typedef float nk_v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 nk_v2bf __attribute__((ext_vector_type(2)));
 
+// Lanes and values. Eight neighbouring lanes own a block of 128 consecutive values, 16 each,
+// as Q pieces of P values that one 16-byte access moves: piece q of lane li (0..7) starts at
+// value 8 P q + P li of the block (bf16: P = 8, Q = 2; fp32: P = 4, Q = 4). Eight lanes'
+// accesses then cover a whole 128-byte line. With 16 consecutive values per lane instead,
+// an access touched every second (fp32: fourth) 16 bytes of twice (four times) the lines,
+// and the streamed lines were fetched again for the next piece.
+template <bool BF16>
+struct Pieces {
+  static constexpr int P = BF16 ? 8 : 4, Q = 16 / P;
+};
+
 // Two fp32 values rounded to bf16 (nearest even, NaN kept), low half first.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(nk_v2f{a, b}, nk_v2bf));
 }
 
-// 16 consecutive values to element idx of a bf16 or fp32 array.
+// A lane's 16 values as loaded, from element idx (its first piece) of an array that is read
+// once; value i as fp32 with [i], i a compile-time constant.
+template <bool BF16>
+struct Raw16 {
+  quant_v4u w[Pieces<BF16>::Q];
+  __device__ __forceinline__ void load(const void* src, int64_t idx) {
+    const quant_v4u* p = BF16 ? (const quant_v4u*)((const uint16_t*)src + idx)
+                              : (const quant_v4u*)((const float*)src + idx);
+#pragma unroll
+    for (int q = 0; q < Pieces<BF16>::Q; ++q) w[q] = __builtin_nontemporal_load(p + 8 * q);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (BF16)
+      return __uint_as_float(i & 1 ? w[i / 8][i / 2 % 4] & 0xFFFF0000u : w[i / 8][i / 2 % 4] << 16);
+    else
+      return __uint_as_float(w[i / 4][i % 4]);
+  }
+};
+
+// A lane's 16 values to element idx (its first piece).
 template <bool BF16>
 __device__ __forceinline__ void store16(void* dst, int64_t idx, const float (&v)[16]) {
   if constexpr (BF16) {
     quant_v4u* p = (quant_v4u*)((uint16_t*)dst + idx);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-      p[q] = quant_v4u{pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                       pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7])};
+      __builtin_nontemporal_store(
+          quant_v4u{pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                    pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7])},
+          p + 8 * q);
   } else {
     nk_v4f* p = (nk_v4f*)((float*)dst + idx);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) p[q] = nk_v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    for (int q = 0; q < 4; ++q)
+      __builtin_nontemporal_store(nk_v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]},
+                                  p + 8 * q);
   }
 }
 
-// 16 consecutive weights (bf16 or fp32, chosen at run time), cached: every row reads them.
-__device__ __forceinline__ void load_weight16(const void* w, int bf16, int64_t idx, float (&v)[16]) {
-  if (bf16) {
-    const quant_v4u* p = (const quant_v4u*)((const uint16_t*)w + idx);
+// A lane's 16 weights at the positions of its values of type BF16, kept as loaded (WBF: bf16
+// weights, else fp32).
+template <bool BF16, bool WBF>
+struct Weight16 {
+  uint32_t w[WBF ? 8 : 16];
+  __device__ __forceinline__ void load(const void* src, int64_t idx) {
+    constexpr int P = Pieces<BF16>::P, D = WBF ? P / 2 : P;  // dwords per piece
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const quant_v4u u = p[q];
+    for (int q = 0; q < Pieces<BF16>::Q; ++q) {
+      const uint32_t* p = WBF ? (const uint32_t*)((const uint16_t*)src + idx + 8 * P * q)
+                              : (const uint32_t*)((const float*)src + idx + 8 * P * q);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * q + 2 * j] = __uint_as_float(u[j] << 16);
-        v[8 * q + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-      }
+      for (int j = 0; j < D; ++j) w[D * q + j] = p[j];
     }
-  } else {
-    const nk_v4f* p = (const nk_v4f*)((const float*)w + idx);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (WBF) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    else return __uint_as_float(w[i]);
+  }
+};
+
+// A lane's 16 fp32 column sums, at the positions of its values of type BF16.
+template <bool BF16>
+__device__ __forceinline__ void store_sums16(float* dst, const float (&v)[16]) {
+  constexpr int P = Pieces<BF16>::P;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const nk_v4f u = p[q];
+  for (int i = 0; i < 16; i += 4)
+    *(nk_v4f*)(dst + i / P * 8 * P + i % P) = nk_v4f{v[i], v[i + 1], v[i + 2], v[i + 3]};
+}
+
+template <bool BF16>
+__device__ __forceinline__ void add_sums16(const float* src, float (&v)[16]) {
+  constexpr int P = Pieces<BF16>::P;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * q + j] = u[j];
-    }
+  for (int i = 0; i < 16; i += 4) {
+    const nk_v4f u = *(const nk_v4f*)(src + i / P * 8 * P + i % P);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[i + j] += u[j];
   }
 }
 
@@ -103,40 +154,88 @@ __device__ __forceinline__ int scale_exp(const ScaleOut& so, float amax) {
   return so.packed && e < -127 ? -127 : e;
 }
 
-// Quantizes 16 values of a 1x128 block that 8 neighbouring lanes hold (li = 0..7 of them),
-// K-block kb of row m: 16 code bytes to codes, the scale by lane li = 0.
+// Data-parallel moves within a wave (v_mov_b32_dpp), without a trip through LDS.
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;  // quad_perm [1,0,3,2], [2,3,0,1]
+constexpr int kDppMirror8 = 0x141, kDppMirror16 = 0x140;  // lane i <- 7 - i, 15 - i
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dppf(float x) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(x)));
+}
+
+// Largest v of 8 neighbouring lanes, in each of them (once the four lanes of a quad agree,
+// the mirrored lane holds the other quad's value).
+__device__ __forceinline__ float max8(float v) {
+  v = fmaxf(v, dppf<kDppXor1>(v));
+  v = fmaxf(v, dppf<kDppXor2>(v));
+  return fmaxf(v, dppf<kDppMirror8>(v));
+}
+
+// Quantizes a lane's 16 values (type BF16's pieces) of the 1x128 block kb of row m. Each lane
+// makes 4 or 8 consecutive codes per piece; neighbouring lanes trade them so that each
+// stores 16 consecutive ones: lane pairs exchange halves (bf16), groups of four lanes
+// transpose their 4x4 words (fp32). The scale is stored by lane li = 0.
+template <bool BF16>
 __device__ __forceinline__ void quantize16(const float (&y)[16], int li, int64_t m, int kb,
                                            uint8_t* codes, const ScaleOut& so) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[i]));
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 8));
-  const int e = scale_exp(so, amax);
-  quant_v4u w;
+  const int e = scale_exp(so, max8(amax));
+  uint32_t w[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     w[q] = quant_e4m3fn_x4(ldexpf(y[4 * q], -e), ldexpf(y[4 * q + 1], -e),
                            ldexpf(y[4 * q + 2], -e), ldexpf(y[4 * q + 3], -e));
-  *(quant_v4u*)(codes + (m * so.KB + kb) * 128 + li * 16) = w;
+  const bool odd = li & 1;
+  int off;
+  quant_v4u out;
+  if constexpr (BF16) {
+    const uint32_t a = dpp<kDppXor1>(odd ? w[0] : w[2]), b = dpp<kDppXor1>(odd ? w[1] : w[3]);
+    out = odd ? quant_v4u{a, b, w[2], w[3]} : quant_v4u{w[0], w[1], a, b};
+    off = odd ? 64 + 8 * (li - 1) : 8 * li;
+  } else {
+    // 2x2 blocks of words, then the words inside them
+    const bool hi = li & 2;
+    const uint32_t a = dpp<kDppXor2>(hi ? w[0] : w[2]), b = dpp<kDppXor2>(hi ? w[1] : w[3]);
+    const uint32_t t0 = hi ? a : w[0], t1 = hi ? b : w[1], t2 = hi ? w[2] : a, t3 = hi ? w[3] : b;
+    const uint32_t c = dpp<kDppXor1>(odd ? t0 : t1), d = dpp<kDppXor1>(odd ? t2 : t3);
+    out = odd ? quant_v4u{c, t1, d, t3} : quant_v4u{t0, c, t2, d};
+    off = 32 * (li & 3) + 4 * (li & 4);
+  }
+  *(quant_v4u*)(codes + (m * so.KB + kb) * 128 + off) = out;
   if (li == 0) store_scale(so, m, kb, e);
 }
 
-// Sum of v over the workgroup, the same in every thread, added in a fixed order. buf: one
-// float per wave, not written again before another barrier has passed (two buffers in turn).
-__device__ __forceinline__ float block_sum(float v, float* buf) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-  const int waves = blockDim.x >> 6;
-  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
-  __syncthreads();
+// Workgroup barrier for LDS traffic only: global loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Sum of v over a row's `waves` waves, of which `wave` is this one, the same in every
+// thread, added in a fixed order. buf: one float per wave of the row, not written again
+// before another barrier has passed (two buffers in turn).
+__device__ __forceinline__ float row_sum(float v, float* buf, int wave, int waves) {
+  v += dppf<kDppXor1>(v);
+  v += dppf<kDppXor2>(v);
+  v += dppf<kDppMirror8>(v);
+  v += dppf<kDppMirror16>(v);
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if ((threadIdx.x & 63) == 0) buf[wave] = v;
+  lds_barrier();
   float s = 0.f;
   for (int i = 0; i < waves; ++i) s += buf[i];
   return s;
 }
 
-constexpr int kNormMaxK = 32768;    // two 16-value chunks in each of 1024 threads
-constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxK = 32768;  // two 16-value chunks in each of 1024 threads
 
 struct NormArgs {
   const void* x;
@@ -149,47 +248,67 @@ struct NormArgs {
   int64_t M;
   int32_t K;
   float eps;
-  int32_t w_bf16;
 };
 
-// Workgroup b takes rows b, b + G, b + 2G, ... (G workgroups); thread t holds the 16 values
-// from column (c * threads + t) * 16 in chunk c < C.
-template <bool BF16, int C>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
-  __shared__ float buf[2][kNormMaxThreads / 64];
-  const int K = a.K, NT = blockDim.x;
-  int par = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, par ^= 1) {
+// First value, in its row, of thread t's chunk c, `threads` threads to a row.
+template <bool BF16>
+__device__ __forceinline__ int norm_col(int c, int threads, int t) {
+  return ((c * threads + t) >> 3) * 128 + (t & 7) * Pieces<BF16>::P;
+}
+
+// Workgroup b takes rows b, b + G, b + 2G, ... (G workgroups), its threads C chunks of 16
+// values each. AHEAD: the weights stay in registers and the next row is loaded before the
+// barrier of this one; otherwise (1024 threads, which leave 128 registers each, fp32) both
+// are loaded where they are used.
+template <bool BF16, bool WBF, int C, int NT, bool AHEAD>
+__global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs a) {
+  __shared__ float buf[2][NT / 64];
+  const int K = a.K, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  int col[C];
+  Weight16<BF16, WBF> w[C];
+  Raw16<BF16> x[C], r[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    col[c] = norm_col<BF16>(c, blockDim.x, threadIdx.x);
+    if (AHEAD && col[c] < K) w[c].load(a.w, col[c]);
+  }
+  auto fetch = [&](int64_t m) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K) {
+        x[c].load(a.x, m * K + col[c]);
+        if (a.r) r[c].load(a.r, m * K + col[c]);
+      }
+  };
+  int64_t m = blockIdx.x;
+  if (AHEAD && m < a.M) fetch(m);
+  for (int par = 0; m < a.M; m += gridDim.x, par ^= 1) {
+    if (!AHEAD) fetch(m);
     float v[C][16];
     float ss = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * NT + (int)threadIdx.x) * 16;
-      if (col < K) {
-        quant_load16<BF16>(a.x, m * K + col, v[c]);
-        if (a.r) {
-          float r[16];
-          quant_load16<BF16>(a.r, m * K + col, r);
+      if (col[c] >= K) continue;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[c][i] += r[i];
-        }
+      for (int i = 0; i < 16; ++i) v[c][i] = x[c][i];
+      if (a.r) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = __builtin_fmaf(v[c][i], v[c][i], ss);
+        for (int i = 0; i < 16; ++i) v[c][i] += r[c][i];
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = __builtin_fmaf(v[c][i], v[c][i], ss);
     }
-    const float rstd = 1.f / sqrtf(block_sum(ss, buf[par]) / (float)K + a.eps);
+    if (AHEAD && m + gridDim.x < a.M) fetch(m + gridDim.x);
+    const float rstd = 1.f / sqrtf(row_sum(ss, buf[par], wave, waves) / (float)K + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[m] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * NT + (int)threadIdx.x) * 16;
-      if (col < K) {
-        if (a.h) store16<BF16>(a.h, m * K + col, v[c]);
-        float w[16];
-        load_weight16(a.w, a.w_bf16, col, w);
+      if (col[c] >= K) continue;
+      if (a.h) store16<BF16>(a.h, m * K + col[c], v[c]);
+      if (!AHEAD) w[c].load(a.w, col[c]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[c][i] = v[c][i] * rstd * w[i];
-        quantize16(v[c], threadIdx.x & 7, m, col >> 7, a.codes, a.so);
-      }
+      for (int i = 0; i < 16; ++i) v[c][i] = v[c][i] * rstd * w[c][i];
+      quantize16<BF16>(v[c], threadIdx.x & 7, m, col[c] >> 7, a.codes, a.so);
     }
   }
 }
@@ -204,66 +323,117 @@ struct NormBwdArgs {
   float* part;     // [gridDim.x][K] partial dweight
   int64_t M;
   int32_t K;
-  int32_t w_bf16;
+  int32_t teams;   // rows that a workgroup works on side by side
 };
 
-// Workgroup b takes rows b, b + G, b + 2G, ... (G workgroups), its threads the columns of
-// rmsnorm_kernel; the weights and the column sums of dweight stay in registers.
-template <bool BF16, int C>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_backward_kernel(NormBwdArgs a) {
-  __shared__ float buf[2][kNormMaxThreads / 64];
-  const int K = a.K, NT = blockDim.x;
-  float w[C][16], dw[C][16];
+// A workgroup is `teams` teams of threads, each on a row of its own (the columns of
+// rmsnorm_kernel); team i of workgroup b takes rows b teams + i + j G teams, j = 0, 1, ...
+// The weights and the column sums of dweight stay in registers; the teams' sums meet in LDS
+// at the end, in team order, so that a workgroup leaves one row of partials. AHEAD: the next
+// row's h and dy are loaded before the barrier of this one, and its dh behind it; otherwise
+// (1024 threads, which leave 128 registers each) a row's values are kept as loaded, and
+// the weights are read again where they are used.
+template <bool BF16, bool WBF, int C, int NT, bool AHEAD>
+__global__ void __launch_bounds__(NT) rmsnorm_backward_kernel(NormBwdArgs a) {
+  __shared__ float buf[2][NT / 64];
+  extern __shared__ float teams_dw[];
+  const int K = a.K, R = a.teams, threads = blockDim.x / R;
+  const int team = threadIdx.x / threads, t = threadIdx.x - team * threads;
+  const int wave = t >> 6, waves = threads >> 6;
+  int col[C];
+  Weight16<BF16, WBF> w[C];
+  float dw[C][16];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * NT + (int)threadIdx.x) * 16;
+    col[c] = norm_col<BF16>(c, threads, t);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[c][i] = 0.f, w[c][i] = 0.f;
-    if (col < K) load_weight16(a.w, a.w_bf16, col, w[c]);
+    for (int i = 0; i < 16; ++i) dw[c][i] = 0.f;
+    if (AHEAD && col[c] < K) w[c].load(a.w, col[c]);
   }
-  int par = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, par ^= 1) {
-    const float rstd = a.rstd[m];
-    float xh[C][16], g[C][16];
-    float dot = 0.f;
+  Raw16<BF16> h[C], dy[C], dh[C];
+  float rs = 0.f;
+  auto fetch = [&](int64_t m) {
+    rs = a.rstd[m];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * NT + (int)threadIdx.x) * 16;
-      if (col < K) {
-        quant_load16<BF16>(a.h, m * K + col, xh[c]);
-        quant_load16<BF16>(a.dy, m * K + col, g[c]);
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K) {
+        h[c].load(a.h, m * K + col[c]);
+        dy[c].load(a.dy, m * K + col[c]);
+      }
+  };
+  auto fetch_dh = [&](int64_t m) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K && a.dh) dh[c].load(a.dh, m * K + col[c]);
+  };
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t m = (int64_t)blockIdx.x * R + team;
+  if (AHEAD && m < a.M) {
+    fetch(m);
+    fetch_dh(m);
+  }
+  // every team passes every barrier: the loop runs while team 0 has a row
+  for (int par = 0; m - team < a.M; m += step, par ^= 1) {
+    const bool live = m < a.M;
+    if (!AHEAD && live) fetch(m);
+    const float rstd = rs;
+    float xh[AHEAD ? C : 1][16], g[AHEAD ? C : 1][16];
+    float dot = 0.f;
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (col[c] >= K) continue;
+        if (!AHEAD) w[c].load(a.w, col[c]);
+        const int k = AHEAD ? c : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          xh[c][i] *= rstd;
-          dw[c][i] = __builtin_fmaf(g[c][i], xh[c][i], dw[c][i]);
-          g[c][i] *= w[c][i];
-          dot = __builtin_fmaf(g[c][i], xh[c][i], dot);
+          const float d = dy[c][i];
+          xh[k][i] = h[c][i] * rstd;
+          dw[c][i] = __builtin_fmaf(d, xh[k][i], dw[c][i]);
+          g[k][i] = d * w[c][i];
+          dot = __builtin_fmaf(g[k][i], xh[k][i], dot);
         }
       }
     }
-    const float mean = block_sum(dot, buf[par]) / (float)K;
+    if (AHEAD && m + step < a.M) fetch(m + step);
+    const float mean = row_sum(dot, buf[par] + team * waves, wave, waves) / (float)K;
+    if (live) {
+      if (!AHEAD) fetch_dh(m);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = (c * NT + (int)threadIdx.x) * 16;
-      if (col < K) {
-        float o[16];
+      for (int c = 0; c < C; ++c) {
+        if (col[c] >= K) continue;
+        const int k = AHEAD ? c : 0;
+        if (!AHEAD) {
+          w[c].load(a.w, col[c]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = rstd * __builtin_fmaf(-xh[c][i], mean, g[c][i]);
-        if (a.dh) {
-          float d[16];
-          quant_load16<BF16>(a.dh, m * K + col, d);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] += d[i];
+          for (int i = 0; i < 16; ++i) xh[k][i] = h[c][i] * rstd, g[k][i] = dy[c][i] * w[c][i];
         }
-        store16<BF16>(a.dx, m * K + col, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          g[k][i] = rstd * __builtin_fmaf(-xh[k][i], mean, g[k][i]);
+          if (a.dh) g[k][i] += dh[c][i];
+        }
+        store16<BF16>(a.dx, m * K + col[c], g[k]);
       }
     }
+    if (AHEAD && m + step < a.M) fetch_dh(m + step);
+  }
+  if (R > 1) {
+    if (team > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (col[c] < K) store_sums16<BF16>(teams_dw + (team - 1) * K + col[c], dw[c]);
+    }
+    __syncthreads();
+    if (team > 0) return;
+    for (int q = 0; q < R - 1; ++q)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (col[c] < K) add_sums16<BF16>(teams_dw + q * K + col[c], dw[c]);
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = (c * NT + (int)threadIdx.x) * 16;
-    if (col < K) store16<false>(a.part, (int64_t)blockIdx.x * K + col, dw[c]);
-  }
+  for (int c = 0; c < C; ++c)
+    if (col[c] < K) store_sums16<BF16>(a.part + (int64_t)blockIdx.x * K + col[c], dw[c]);
 }
 
 struct ActBwdArgs {
@@ -279,57 +449,74 @@ struct ActBwdArgs {
   int32_t strips;       // column strips of 1024
 };
 
-// A workgroup of four waves takes a strip of 1024 columns (64 lanes of 16) over a group of
-// rows, wave w rows w, w + 4, ... of the group; the waves' column sums meet in LDS.
+// A workgroup of four waves takes a strip of 1024 columns (8 blocks of 128, 8 lanes each)
+// over a group of rows, wave w rows w, w + 4, ... of the group, the next row's loads in
+// flight; the waves' column sums meet in LDS.
 __global__ void __launch_bounds__(256) act_backward_kernel(ActBwdArgs a) {
-  __shared__ float sums[4][1024];
+  __shared__ float sums[3][1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int strip = blockIdx.x % a.strips, group = blockIdx.x / a.strips;
-  const int col = strip * 1024 + lane * 16;
+  const int in_strip = (lane >> 3) * 128 + (lane & 7) * Pieces<true>::P;
+  const int col = strip * 1024 + in_strip;
+  const bool has_pre = a.act != DG_ACT_NONE;
   const int64_t m1 = min(a.M, (group + 1) * a.rows);
   float sum[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) sum[i] = 0.f;
   if (col < a.N) {
-    for (int64_t m = group * a.rows + wave; m < m1; m += 4) {
-      float d[16];
-      quant_load16<true>(a.dc, m * a.N + col, d);
-      if (a.act != DG_ACT_NONE) {
-        float x[16];
-        quant_load16<true>(a.pre, m * a.N + col, x);
-        act_backward(d, x, a.act);
-      }
+    Raw16<true> d, x;
+    auto fetch = [&](int64_t m) {
+      if (m >= m1) return;
+      d.load(a.dc, m * a.N + col);
+      if (has_pre) x.load(a.pre, m * a.N + col);
+    };
+    int64_t m = group * a.rows + wave;
+    fetch(m);
+    for (; m < m1; m += 4) {
+      float p[16], z[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum[i] += d[i];
-      quantize16(d, lane & 7, m, col >> 7, a.codes, a.so);
+      for (int i = 0; i < 16; ++i) p[i] = d[i], z[i] = has_pre ? x[i] : 0.f;
+      fetch(m + 4);
+      act_backward(p, z, a.act);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i] += p[i];
+      quantize16<true>(p, lane & 7, m, col >> 7, a.codes, a.so);
     }
   }
   if (!a.part) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) sums[wave][lane * 16 + i] = sum[i];
+  if (wave > 0) store_sums16<true>(sums[wave - 1] + in_strip, sum);
   __syncthreads();
-  for (int i = threadIdx.x; i < 1024; i += 256)
-    if (strip * 1024 + i < a.N)
-      a.part[(int64_t)group * a.N + strip * 1024 + i] =
-          (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+  if (wave > 0 || col >= a.N) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) add_sums16<true>(sums[w] + in_strip, sum);
+  store_sums16<true>(a.part + (int64_t)group * a.N + col, sum);
 }
 
-// out[n] = sum of the R partial rows part[.][n], n < N (N % 16 == 0): 16 columns per
-// workgroup, thread (q, r) adds rows r, r + 64, ... of columns 4q .. 4q+3, and the 64 row
-// sums are added pairwise in LDS.
+// out[n] = sum of the R partial rows part[.][n], n < N (N % 32 == 0): a workgroup takes 32
+// columns (a 128-byte line of each row), thread (q, r) rows r, r + 32, ... of columns
+// 4q .. 4q+3 with eight loads in flight (past the last row: the last row again, not added),
+// and the 32 row sums are added pairwise in LDS.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, float* out, int R, int N) {
-  __shared__ nk_v4f s[64][4];
-  const int q = threadIdx.x & 3, r = threadIdx.x >> 2;
-  const int col = blockIdx.x * 16 + q * 4;
+  __shared__ nk_v4f s[32][8];
+  constexpr int U = 8;
+  const int q = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + q * 4;
   nk_v4f sum = {0.f, 0.f, 0.f, 0.f};
-  for (int i = r; i < R; i += 64) {
-    const nk_v4f v = *(const nk_v4f*)(part + (int64_t)i * N + col);
-    for (int j = 0; j < 4; ++j) sum[j] += v[j];
+  for (int i = r; i < R; i += 32 * U) {
+    nk_v4f v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = *(const nk_v4f*)(part + (int64_t)min(i + 32 * u, R - 1) * N + col);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += i + 32 * u < R ? v[u][j] : 0.f;
   }
   s[r][q] = sum;
-  for (int d = 32; d >= 1; d >>= 1) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
     __syncthreads();
     if (r < d) {
+#pragma unroll
       for (int j = 0; j < 4; ++j) sum[j] += s[r + d][q][j];
       s[r][q] = sum;
     }
