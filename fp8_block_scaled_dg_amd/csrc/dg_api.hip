@@ -28,6 +28,7 @@
 #include "norm_kernel.hpp"
 #include "pipe_kernel.hpp"
 #include "quant_kernel.hpp"
+#include "ring_kernel.hpp"
 #include "skinny_kernel.hpp"
 #include "stream_kernel.hpp"
 #include "transpose_kernel.hpp"
@@ -361,25 +362,24 @@ int tile_group(int64_t tiles) {
   return 1;
 }
 
-template <class Cfg, int LAY, int EPI>
-dg_status launch_skinny_as(const Problem& p0, const Epilogue& ep, hipStream_t stream) {
+template <class Cfg, int LAY = 0>
+dg_status launch_skinny(const Problem& p0, int64_t blocks, hipStream_t stream) {
+  (void)blocks;
   if (LAY != 0 && p0.sfa_packed) return fail(DG_ERR_UNSUPPORTED_SHAPE, "packed sfA with MN-contiguous operands");
-  constexpr int lds_slots = (LAY & kLayBN) ? Cfg::LDS_BYTES_BN : Cfg::LDS_BYTES;
-  constexpr int lds_bytes = EPI != kEpiNone && Cfg::LDS_EPI > lds_slots ? Cfg::LDS_EPI : lds_slots;
+  constexpr int lds_bytes = (LAY & kLayBN) ? Cfg::LDS_BYTES_BN : Cfg::LDS_BYTES;
   static std::once_flag once;
   static hipError_t attr_err = hipSuccess;
   std::call_once(once, [] {
-    attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, false, LAY, EPI>,
+    attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, false, LAY>,
                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
     if (attr_err == hipSuccess && LAY == 0)
-      attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, true, 0, EPI>,
+      attr_err = hipFuncSetAttribute((const void*)skinny_kernel<Cfg, true>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
   });
   if (attr_err != hipSuccess)
     return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(attr_err));
   SkinnyArgs a{};
   a.p = p0;
-  a.ep = ep;
   const int KB = (int)(p0.K / kKBlock);
   const int64_t tiles = (p0.N + Cfg::BN - 1) / Cfg::BN;
   // K splits: as many as keep the grid within one workgroup per CU (a grid slightly
@@ -407,23 +407,17 @@ dg_status launch_skinny_as(const Problem& p0, const Epilogue& ep, hipStream_t st
     if (st != DG_OK) return st;
   }
   if (LAY != 0)
-    hipLaunchKernelGGL((skinny_kernel<Cfg, false, LAY, EPI>), dim3((unsigned)grid), dim3(Cfg::NT),
+    hipLaunchKernelGGL((skinny_kernel<Cfg, false, LAY>), dim3((unsigned)grid), dim3(Cfg::NT),
                        lds_bytes, stream, a);
   else if (p0.sfa_packed)
-    hipLaunchKernelGGL((skinny_kernel<Cfg, true, 0, EPI>), dim3((unsigned)grid), dim3(Cfg::NT),
+    hipLaunchKernelGGL((skinny_kernel<Cfg, true>), dim3((unsigned)grid), dim3(Cfg::NT),
                        lds_bytes, stream, a);
   else
-    hipLaunchKernelGGL((skinny_kernel<Cfg, false, 0, EPI>), dim3((unsigned)grid), dim3(Cfg::NT),
+    hipLaunchKernelGGL((skinny_kernel<Cfg, false>), dim3((unsigned)grid), dim3(Cfg::NT),
                        lds_bytes, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
   return DG_OK;
-}
-
-template <class Cfg, int LAY = 0>
-dg_status launch_skinny(const Problem& p, int64_t blocks, hipStream_t stream) {
-  (void)blocks;
-  return launch_skinny_as<Cfg, LAY, kEpiNone>(p, Epilogue{}, stream);
 }
 
 // ---------------------------------------------------------------- stream kernel
@@ -457,14 +451,14 @@ bool stream_fits(int64_t M, int64_t N, int64_t K) {
   return stream_plan<Cfg>(N, K).KS <= Cfg::D;
 }
 
-template <class Cfg, int LAY, int EPI>
-dg_status launch_stream_as(const Problem& p0, const Epilogue& ep, hipStream_t stream) {
+template <class Cfg, int LAY = 0>
+dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
+  (void)blocks;
   if (LAY != 0 && p0.sfa_packed) return fail(DG_ERR_UNSUPPORTED_SHAPE, "packed sfA with MN-contiguous operands");
   const StreamPlan pl = stream_plan<Cfg, LAY>(p0.N, p0.K);
   if (pl.KS > Cfg::D) return fail(DG_ERR_UNSUPPORTED_SHAPE, "K run %lld > %d", (long long)pl.KS, Cfg::D);
   StreamArgs a{};
   a.p = p0;
-  a.ep = ep;
   a.S = (int32_t)pl.S;
   a.KS = (int32_t)pl.KS;
   a.tiles = (int32_t)pl.tiles;
@@ -476,20 +470,86 @@ dg_status launch_stream_as(const Problem& p0, const Epilogue& ep, hipStream_t st
     if (st != DG_OK) return st;
   }
   if (LAY != 0)
-    hipLaunchKernelGGL((stream_kernel<Cfg, false, LAY, EPI>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
+    hipLaunchKernelGGL((stream_kernel<Cfg, false, LAY>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
   else if (p0.sfa_packed)
-    hipLaunchKernelGGL((stream_kernel<Cfg, true, 0, EPI>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
+    hipLaunchKernelGGL((stream_kernel<Cfg, true>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
   else
-    hipLaunchKernelGGL((stream_kernel<Cfg, false, 0, EPI>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
+    hipLaunchKernelGGL((stream_kernel<Cfg, false>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
   return DG_OK;
 }
 
-template <class Cfg, int LAY = 0>
-dg_status launch_stream(const Problem& p, int64_t blocks, hipStream_t stream) {
-  (void)blocks;
-  return launch_stream_as<Cfg, LAY, kEpiNone>(p, Epilogue{}, stream);
+// ---------------------------------------------------------------- ring kernel
+
+// The K split of the ring kernel: the S <= 8 with at most one workgroup per CU that
+// minimises, in units of 0.1 us, the time of a run of pairs of K-blocks plus, for S > 1, the
+// partials' trip through memory and the last split's sum over them. Fitted to measurements on
+// one MI355X; TM is the number of 16-row tiles. E.g. FP8 output, M = 64: 4096 columns,
+// K = 7168, S = 1 / 2 / 4 / 8: 27.2 / 19.5 / 15.6 / 16.2 us; 8192 columns, K = 2048, S = 1 /
+// 2 / 4: 12.2 / 12.6 / 14.7 us; M = 1, 2048 columns, K = 4096, S = 1 / 2 / 4 / 8: 10.7 / 8.9 /
+// 8.0 / 7.8 us.
+struct RingPlan {
+  int64_t S, KS;
+};
+
+RingPlan ring_plan(int64_t tiles, int64_t KB, int tm) {
+  const double pair = tm == 4 ? 8 : tm == 2 ? 6 : 4.5, fixed = tm == 4 ? 25 : tm == 2 ? 18 : 12,
+               each = tm == 4 ? 7.5 : tm == 2 ? 4 : 2.2;
+  const int64_t pairs = (KB + 1) / 2;
+  RingPlan best{1, KB};
+  double least = pair * (double)pairs;
+  for (int64_t S = 2; S <= 8 && S <= pairs && tiles * S <= kCUs; ++S) {
+    const int64_t run = (pairs + S - 1) / S, used = (pairs + run - 1) / run;
+    const double t = pair * (double)run + fixed + each * (double)used;
+    if (t < least) least = t, best = RingPlan{used, 2 * run};
+  }
+  return best;
+}
+
+template <class Cfg, int EPI>
+dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t stream) {
+  static_assert(Cfg::SMAX >= 8, "ring_plan's splits");
+  RingArgs a{};
+  a.p = p;
+  a.ep = ep;
+  const int64_t tiles = (p.N + Cfg::BN - 1) / Cfg::BN;
+  const RingPlan pl = ring_plan(tiles, p.K / kKBlock, Cfg::BM / 16);
+  a.S = (int32_t)pl.S;
+  a.KS = (int32_t)pl.KS;
+  const int64_t grid = tiles * pl.S;
+  if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld", (long long)grid);
+  if (pl.S > 1) {
+    const size_t part = (size_t)grid * Cfg::BM * Cfg::BN * sizeof(float);
+    const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
+    if (st != DG_OK) return st;
+  }
+  hipLaunchKernelGGL((ring_kernel<Cfg, EPI>), dim3((unsigned)grid), dim3(Cfg::NT), 0, stream, a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
+  return DG_OK;
+}
+
+// The forms by rows and sfA layout. WIDE: 4 waves, 128 columns, B streamed past the caches;
+// otherwise 8 waves (4 for 64 columns and at most 16 rows) and BN columns.
+template <int BN, bool WIDE, int EPI, bool PACKED>
+dg_status launch_ring_rows(const Problem& p, const Epilogue& ep, hipStream_t st) {
+  if constexpr (WIDE) {
+    if (p.M <= 16) return launch_ring_as<RingCfg<4, 1, 1, 2, 3, PACKED, true>, EPI>(p, ep, st);
+    if (p.M <= 32) return launch_ring_as<RingCfg<4, 1, 2, 2, 3, PACKED, true>, EPI>(p, ep, st);
+    return launch_ring_as<RingCfg<4, 1, 4, 2, 3, PACKED, true>, EPI>(p, ep, st);
+  } else {
+    constexpr int W1 = BN == 64 ? 4 : 8, TN = BN / 64;
+    if (p.M <= 16) return launch_ring_as<RingCfg<W1, 1, 1, BN / 16 / W1, 3, PACKED, false>, EPI>(p, ep, st);
+    if (p.M <= 32) return launch_ring_as<RingCfg<8, 2, 1, TN, 3, PACKED, false>, EPI>(p, ep, st);
+    return launch_ring_as<RingCfg<8, 2, 2, TN, 3, PACKED, false>, EPI>(p, ep, st);
+  }
+}
+
+template <int BN, bool WIDE, int EPI>
+dg_status launch_ring(const Problem& p, const Epilogue& ep, hipStream_t st) {
+  return p.sfa_packed ? launch_ring_rows<BN, WIDE, EPI, true>(p, ep, st)
+                      : launch_ring_rows<BN, WIDE, EPI, false>(p, ep, st);
 }
 
 using Stream1x10 = StreamCfg<4, 1, 10>;
@@ -539,31 +599,33 @@ const CfgEntry kTable[] = {
      launch_pipe128<kMasked>, 0, kPipeMaxKB, nullptr, launch_pipe128_epi<kEpiBf16>,
      launch_pipe128_epi<kEpiFp8>},
     {"skinny_w4_tn1_d3", launch_skinny<SkinnyCfg<4, 1, 3>>, nullptr, nullptr, 64, 0},
-    {"skinny_w4_tn1_d2", launch_skinny<SkinnyCfg<4, 1, 2>>, nullptr, nullptr, 64, 0, nullptr,
-     launch_skinny_as<SkinnyCfg<4, 1, 2>, 0, kEpiBf16>},
+    {"skinny_w4_tn1_d2", launch_skinny<SkinnyCfg<4, 1, 2>>, nullptr, nullptr, 64, 0},
     {"skinny_w4_tn1_d5", launch_skinny<SkinnyCfg<4, 1, 5>>, nullptr, nullptr, 64, 0},
-    {"skinny_w4_tn1_d8", launch_skinny<SkinnyCfg<4, 1, 8>>, nullptr, nullptr, 64, 0, nullptr,
-     launch_skinny_as<SkinnyCfg<4, 1, 8>, 0, kEpiBf16>},
+    {"skinny_w4_tn1_d8", launch_skinny<SkinnyCfg<4, 1, 8>>, nullptr, nullptr, 64, 0},
     {"skinny_w2_tn1_d3", launch_skinny<SkinnyCfg<2, 1, 3>>, nullptr, nullptr, 64, 0},
     {"skinny_w2_tn1_d5", launch_skinny<SkinnyCfg<2, 1, 5>>, nullptr, nullptr, 64, 0},
     {"skinny_w2_tn1_d8", launch_skinny<SkinnyCfg<2, 1, 8>>, nullptr, nullptr, 64, 0},
-    {"skinny_w8_tn1_d4", launch_skinny<SkinnyCfg<8, 1, 4>>, nullptr, nullptr, 64, 0, nullptr,
-     nullptr, launch_skinny_as<SkinnyCfg<8, 1, 4>, 0, kEpiFp8>},
-    {"skinny_w8_tn1_d2", launch_skinny<SkinnyCfg<8, 1, 2>>, nullptr, nullptr, 64, 0, nullptr,
-     nullptr, launch_skinny_as<SkinnyCfg<8, 1, 2>, 0, kEpiFp8>},
+    {"skinny_w8_tn1_d4", launch_skinny<SkinnyCfg<8, 1, 4>>, nullptr, nullptr, 64, 0},
+    {"skinny_w8_tn1_d2", launch_skinny<SkinnyCfg<8, 1, 2>>, nullptr, nullptr, 64, 0},
     {"skinny_w2_tn1_d2", launch_skinny<SkinnyCfg<2, 1, 2>>, nullptr, nullptr, 64, 0},
     {"stream_w4_tn1_d10", launch_stream<Stream1x10>, nullptr, nullptr, 64, 0,
-     stream_fits<Stream1x10>, launch_stream_as<Stream1x10, 0, kEpiBf16>},
+     stream_fits<Stream1x10>},
     {"stream_w4_tn2_d4", launch_stream<Stream2x4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream2x4>},
     {"stream_w4_tn1_d4", launch_stream<Stream1x4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream1x4>},
     {"stream_w8_tn1_d10", launch_stream<Stream8w10>, nullptr, nullptr, 64, 0,
-     stream_fits<Stream8w10>, nullptr, launch_stream_as<Stream8w10, 0, kEpiFp8>},
+     stream_fits<Stream8w10>},
     {"stream_w8_tn1_d4", launch_stream<Stream8w4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream8w4>},
     {"stream_w2_tn1_d4", launch_stream<Stream2w4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream2w4>},
+    // M <= 64 with a fused epilogue
+    {"ring_n64", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr, launch_ring<64, false, kEpiBf16>},
+    {"ring_n128", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr, nullptr,
+     launch_ring<128, false, kEpiFp8>},
+    {"ring_n128_wide", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr,
+     launch_ring<128, true, kEpiBf16>, launch_ring<128, true, kEpiFp8>},
 };
 constexpr int kNumCfg = (int)(sizeof(kTable) / sizeof(kTable[0]));
 
@@ -619,33 +681,34 @@ int select_config(int kind, int64_t m, int64_t M, int64_t n, int64_t k, int32_t 
   return find_cfg("pipe128x256");
 }
 
-// The same for the dense GEMM with a fused epilogue; -1 when K is beyond the kernels that
-// have one. bf16 output: select_config's choice. FP8 output: M <= 64 needs 128-column
-// workgroups, so that one workgroup holds whole 1x128 blocks of a row.
+// From this many bytes on, B is streamed past the caches: the 256 MB MALL cannot be expected
+// to hold it from one use to the next. M = 64, FP8 output, 18432 x 7168 (132 MB): 35.8 us
+// streamed, 40.2 not; 4096 x 7168 (29 MB), read over and over: 17.9 us streamed, 15.6 not.
+constexpr int64_t kStreamB = int64_t(96) << 20;
+
+// Rows from which on the tile kernel's 128x256 tiles serve a product with a fused epilogue.
+constexpr int64_t kRingRows = 64;
+
+// The configuration of the dense GEMM with a fused epilogue; -1 when K is beyond the kernels
+// that have one. FP8 output on M <= 64 needs 128-column workgroups, so that one workgroup
+// holds whole 1x128 blocks of a row; bf16 output gets 64-column ones, twice as many.
 int select_epi_config(bool fp8, int64_t M, int64_t N, int64_t K) {
   const auto has = [&](int id) {
-    return (fp8 ? kTable[id].bias_act_fp8 : kTable[id].bias_act) && cfg_applies(id, kDense, M, N, K);
+    const CfgEntry& c = kTable[id];
+    return (fp8 ? c.bias_act_fp8 : c.bias_act) && (!c.max_m || M <= c.max_m) &&
+           (!c.max_kb || K / kKBlock <= c.max_kb);
   };
   const char* forced = getenv("DG_FORCE_CONFIG");
   if (forced && *forced) {
     const int id = find_cfg(forced);
     if (id >= 0 && has(id)) return id;
   }
-  const int64_t KB = K / kKBlock;
-  if (M > 64) {
-    if (KB > kPipeMaxKB) return -1;
-    return find_cfg(M <= 128 && (N + 255) / 256 < 8 ? "pipe256x128" : "pipe128x256");
-  }
-  const int BN = fp8 ? 128 : 64;
-  const int s1 = find_cfg(fp8 ? "stream_w8_tn1_d10" : "stream_w4_tn1_d10");
-  if (KB >= 16 && has(s1)) return s1;
-  const int64_t tiles = (N + BN - 1) / BN;
-  int64_t s = kCUs / tiles;
-  s = s > 8 ? 8 : (s < 1 ? 1 : s);
-  if (s > KB) s = KB;
-  const bool deep = (KB + s - 1) / s >= 6;
-  return find_cfg(fp8 ? (deep ? "skinny_w8_tn1_d4" : "skinny_w8_tn1_d2")
-                      : (deep ? "skinny_w4_tn1_d8" : "skinny_w4_tn1_d2"));
+  int id;
+  if (M <= kRingRows)
+    id = find_cfg(N * K >= kStreamB ? "ring_n128_wide" : fp8 ? "ring_n128" : "ring_n64");
+  else
+    id = find_cfg(M <= 128 && (N + 255) / 256 < 8 ? "pipe256x128" : "pipe128x256");
+  return has(id) ? id : -1;
 }
 
 bool print_configs() {
@@ -1143,7 +1206,7 @@ dg_status gemm_epilogue(const void* A, const void* B, const void* sfA, int32_t s
   if (M > (int64_t)1 << 30) return fail(DG_ERR_UNSUPPORTED_SHAPE, "M beyond 2^30");
   const int id = select_epi_config(fp8, M, N, K);
   if (id < 0)
-    return fail(DG_ERR_UNSUPPORTED_SHAPE, "K=%lld with M > 64: the fused epilogues go up to K = %lld",
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "K=%lld: the fused epilogues go up to K = %lld",
                 (long long)K, (long long)kPipeMaxKB * kKBlock);
   maybe_print(kDense, M, N, K, 1, id, fp8 ? " (fused epilogue, FP8 output)" : " (fused epilogue)");
   Problem p{};

@@ -71,24 +71,25 @@ __device__ __forceinline__ void epi_store8(v4u res, uint16_t* C, int64_t off, fl
   __builtin_nontemporal_store(epi_pack8(v), (v4u*)(C + off));
 }
 
-// Row pitch, in floats, of the fp32 tile that the M <= 64 kernels leave in LDS: 4 floats
+// Row pitch, in floats, of the fp32 tile that the M <= 64 kernel leaves in LDS: 4 floats
 // past BN spread the rows over the banks.
 template <int BN>
 constexpr int kEpiPitch = BN + 4;
 
-// Finishes the fp32 tile out[64][kEpiPitch<BN>] of columns n0 .. n0 + BN - 1 (all threads of
-// the workgroup, after a barrier): 8 columns of a row per thread and step. kEpiFp8: BN = 128,
-// 16 neighbouring lanes hold a row's 1x128 block.
-template <int BN, int NT, int EPI>
+// Finishes rows row0 .. row0 + ROWS - 1 of the fp32 tile of columns n0 .. n0 + BN - 1, held
+// in out[ROWS][kEpiPitch<BN>] (all threads of the workgroup, after a barrier): 8 columns of
+// a row per thread and step. kEpiFp8: BN = 128, 16 neighbouring lanes hold a row's 1x128
+// block.
+template <int BN, int NT, int EPI, int ROWS>
 __device__ __forceinline__ void epi_finish_tile(const Problem& p, int64_t n0, const float* out,
-                                                const Epilogue& ep) {
+                                                const Epilogue& ep, int row0) {
   static_assert(EPI != kEpiFp8 || BN == 128, "a scale block per tile row");
   constexpr int LPR = BN / 8;  // lanes per row
-  static_assert(64 % LPR == 0 && (64 * LPR) % NT == 0, "whole rows per wave");
+  static_assert(64 % LPR == 0 && (ROWS * LPR) % 64 == 0, "whole rows per wave");
   const int64_t N = p.N;
 #pragma unroll 1
-  for (int c = threadIdx.x; c < 64 * LPR; c += NT) {
-    const int row = c / LPR, col0 = (c % LPR) * 8;
+  for (int c = threadIdx.x; c < ROWS * LPR; c += NT) {
+    const int rl = c / LPR, row = row0 + rl, col0 = (c % LPR) * 8;
     const int64_t col = n0 + col0, off = row * N + col;
     if (row >= p.M || col >= N) continue;
     v4u res = {0, 0, 0, 0};
@@ -96,8 +97,8 @@ __device__ __forceinline__ void epi_finish_tile(const Problem& p, int64_t n0, co
       res = __builtin_nontemporal_load((const v4u*)(ep.residual + off));
     float b[8], x[8];
     epi_bias8(ep, col, b);
-    const v4f lo = *(const v4f*)(out + row * kEpiPitch<BN> + col0);
-    const v4f hi = *(const v4f*)(out + row * kEpiPitch<BN> + col0 + 4);
+    const v4f lo = *(const v4f*)(out + rl * kEpiPitch<BN> + col0);
+    const v4f hi = *(const v4f*)(out + rl * kEpiPitch<BN> + col0 + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
     epi_act8(ep, b, off, x);

@@ -41,7 +41,6 @@
 //     128-byte line shared with a neighbouring tile.
 #pragma once
 
-#include "epilogue.hpp"
 #include "gemm_kernel.hpp"
 
 namespace dg {
@@ -57,7 +56,6 @@ struct SkinnyCfg {
   static constexpr int LDS_BYTES = D * SLOT;
   static constexpr int SLOT_BN = SLOT + 128 * 64;      // + B tile stored [K][N]
   static constexpr int LDS_BYTES_BN = D * SLOT_BN;
-  static constexpr int LDS_EPI = 64 * kEpiPitch<BN> * 4;  // fp32 tile of the EPI kernels (likewise)
   static constexpr int LDS_OUT = 64 * BN * 2;  // bf16 output staging (aliases the slots)
   static_assert(512 % NT == 0, "A chunks split evenly over the threads");
   static_assert(LDS_OUT <= LDS_BYTES, "output staging fits in the pipeline slots");
@@ -73,7 +71,6 @@ struct SkinnyArgs {
   int32_t KS;          // K-blocks per split (the last split may have fewer)
   int32_t tiles;       // column tiles
   int32_t group;       // B stored [K][N]: consecutive column tiles per XCD group
-  Epilogue ep;         // bias, activation, residual or quantization (EPI kernels)
 };
 
 // Registers of one block in flight.
@@ -170,7 +167,7 @@ __device__ __forceinline__ void skinny_mma(v4f (&acc)[Cfg::TM][Cfg::TN], const u
 // PACKED: sfA in the packed UE8M0 layout (a compile-time choice, so that the fp32
 // form carries no trace of it). LAY: kLayAT / kLayBN bits, the operands stored
 // MN-contiguous.
-template <class Cfg, bool PACKED, int LAY = 0, int EPI = kEpiNone>
+template <class Cfg, bool PACKED, int LAY = 0>
 __global__ void __launch_bounds__(Cfg::NT) skinny_kernel(SkinnyArgs args) {
   static_assert(LAY == 0 || (Cfg::W == 4 && Cfg::TN == 1),
                 "MN-contiguous operands: 64-column workgroups of 4 waves");
@@ -353,22 +350,6 @@ __global__ void __launch_bounds__(Cfg::NT) skinny_kernel(SkinnyArgs args) {
       }
     if (tid == 0)
       __hip_atomic_store(&args.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-
-  // ---- bias, activation and residual or quantization on the fp32 tile (epilogue.hpp)
-  if constexpr (EPI != kEpiNone) {
-    __syncthreads();
-    float* out = (float*)lds;
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          out[(i * 16 + 4 * g + q) * kEpiPitch<BN> + (wave * TN + j) * 16 + l16] = acc[i][j][q];
-    __syncthreads();
-    epi_finish_tile<BN, NT, EPI>(p, n0, out, args.ep);
-    return;
   }
 
   // ---- bf16 through LDS (aliases the pipeline slots), 16-byte stores

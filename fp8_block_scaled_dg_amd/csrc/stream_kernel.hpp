@@ -43,7 +43,6 @@
 //     follow it.
 #pragma once
 
-#include "epilogue.hpp"
 #include "gemm_kernel.hpp"
 
 namespace dg {
@@ -68,8 +67,6 @@ template <int I>
 __shared__ __align__(16) uint8_t stream_a[64 * kKBlock];  // A tile of block I
 __shared__ __align__(16) uint8_t stream_sfa[3 * 1024];     // sfA: [group][row][4]
 __shared__ __align__(16) uint16_t stream_out[64 * 128];    // bf16 output staging
-template <int BN>
-__shared__ __align__(16) float stream_epi[64 * kEpiPitch<BN>];  // fp32 tile (EPI kernels)
 __shared__ __align__(16) uint8_t stream_bt[6][128 * 64];   // B stored [K][N]: two 3-block sets
 
 struct StreamArgs {
@@ -80,7 +77,6 @@ struct StreamArgs {
   int32_t KS;          // K-blocks per split (the last split may have fewer)
   int32_t tiles;
   int32_t group;       // consecutive column tiles per XCD group (workgroup mapping)
-  Epilogue ep;         // bias, activation, residual or quantization (EPI kernels)
 };
 
 template <class Cfg>
@@ -228,7 +224,7 @@ __device__ __forceinline__ void stream_compute(v4f (&acc)[Cfg::TM][Cfg::TN], con
 
 // PACKED: sfA in the packed UE8M0 layout (compile-time, as in the skinny kernel).
 // LAY: kLayAT / kLayBN bits, the operands stored MN-contiguous.
-template <class Cfg, bool PACKED, int LAY = 0, int EPI = kEpiNone>
+template <class Cfg, bool PACKED, int LAY = 0>
 __global__ void __launch_bounds__(Cfg::NT) stream_kernel(StreamArgs args) {
   static_assert(LAY == 0 || (Cfg::W == 4 && Cfg::TN == 1),
                 "MN-contiguous operands: 64-column workgroups of 4 waves");
@@ -405,19 +401,6 @@ __global__ void __launch_bounds__(Cfg::NT) stream_kernel(StreamArgs args) {
       }
     if (tid == 0)
       __hip_atomic_store(&args.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-
-  // ---- bias, activation and residual or quantization on the fp32 tile (epilogue.hpp)
-  if constexpr (EPI != kEpiNone) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        *(v4f*)(stream_epi<BN> + (i * 16 + l16) * kEpiPitch<BN> + (wave * TN + j) * 16 + 4 * g) =
-            acc[i][j];
-    __syncthreads();
-    epi_finish_tile<BN, NT, EPI>(p, n0, stream_epi<BN>, args.ep);
-    return;
   }
 
   // ---- bf16 through LDS, 16-byte stores. Lane (g, l16) of tile (i, j) holds row

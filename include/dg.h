@@ -326,7 +326,7 @@ typedef enum dg_activation {
  *   pre       bf16 [M][N], for the backward of the activation; NULL: not stored
  *   sfA       fp32 [M][K/128], or with sfA_packed != 0 packed UE8M0 words
  * Every value is rounded once. Shapes, alignment (bias, residual and pre 16 bytes), stream,
- * workspace and error rules of dg_fp8_gemm_nt; with M > 64, K <= 2^22.
+ * workspace and error rules of dg_fp8_gemm_nt, and K <= 2^22.
  */
 dg_status dg_fp8_gemm_nt_bias_act(const void* A, const void* B, void* C, const void* sfA,
                                   int32_t sfA_packed, const float* sfB, const void* bias,

@@ -5,9 +5,9 @@ oracle's exact product and the definitions in 64 bits (tests/_ops64.py).
 Integer-valued operands make the product exact in fp32, so that without an activation the
 bf16 output has one possible value (bias and residual chosen so that their sums are exact
 too), and with one its distance is the activation's. N(0,1) operands add the product's own
-error model. Every kernel that serves the calls is reached: both M <= 64 kernels with and
-without split K, the compute-bound kernel's tiles, its K-split tail tiles, both scale
-forms; odd M, N tails inside a tile, one row, one K-block."""
+error model. Every kernel that serves the calls is reached: the M <= 64 kernel in each of
+its forms, with and without split K, the compute-bound kernel's tiles, its K-split tail
+tiles, both scale forms; odd M, N tails inside a tile, one row, one K-block."""
 import numpy as np
 import pytest
 import torch
@@ -176,9 +176,35 @@ def test_normal_operands(M, N, K):
           f"normal {M}x{N}x{K}", strict=False)
 
 
-@pytest.mark.parametrize("M,N,K", [(64, 2112, 7168), (9, 4096, 512), (130, 2112, 2048), (1000, 1024, 512)])
+@pytest.mark.parametrize("config", ["ring_n64", "ring_n128", "ring_n128_wide"])
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("N,KB", [(128, 1), (256, 2), (384, 3), (128, 5), (1040, 6), (512, 7), (256, 13), (128, 40)])
+def test_row_counts_and_run_lengths(monkeypatch, config, M, N, KB):
+    """The M <= 64 kernel: every number of 16-row tiles, runs of K-blocks that end in each
+    stage of its ring, with and without an odd last block, and N tails."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", config)
+    fp8 = config != "ring_n64" and N % 128 == 0
+    packed = (M + KB) % 2 == 0
+    A, B, sfA, sfB, r = operands(M, N, 128 * KB, M + N + KB)
+    a, b, sa, sb = gu.codes(A), gu.codes(B), pack(sfA) if packed else gu.dev(sfA), gu.dev(sfB)
+    if config != "ring_n128":
+        out = gu.Guarded((M, N), 5)
+        gu.announce(f"{config} M={M} N={N} KB={KB}")
+        dg().fp8_gemm_nt_bias_act(a, b, out.out, sa, sb)
+        torch.cuda.synchronize()
+        assert out.guards_intact() and np.array_equal(out.result(), oracle.bf16_rne(r))
+    if fp8:
+        out = Fp8Out(M, N, not packed)
+        gu.announce(f"{config} FP8 M={M} N={N} KB={KB}")
+        dg().fp8_gemm_nt_bias_act_fp8(a, b, sa, sb, codes=out.codes, sf=out.sf)
+        codes, sf = out.result()
+        rc, rs = oracle.quantize_blocks(r.astype(np.float32), 1, 128)
+        assert np.array_equal(rs, sf) and np.array_equal(rc, codes)
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 2112, 2048), (1000, 1024, 512)])
 def test_plain_call_and_no_epilogue_agree(M, N, K):
-    # nothing to add: the same bits as the plain call, whose kernels these are
+    # nothing to add: the same bits as the plain call, whose kernel this is
     rng = np.random.default_rng(13)
     A, sfA = oracle.quantize_blocks(rng.normal(size=(M, K)).astype(np.float32), 1, 128)
     B, sfB = oracle.quantize_blocks(rng.normal(size=(N, K)).astype(np.float32), 128, 128)
