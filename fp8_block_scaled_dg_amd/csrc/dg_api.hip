@@ -482,39 +482,60 @@ dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
 
 // ---------------------------------------------------------------- ring kernel
 
-// The K split of the ring kernel: the S <= 8 with at most one workgroup per CU that
-// minimises, in units of 0.1 us, the time of a run of pairs of K-blocks plus, for S > 1, the
-// partials' trip through memory and the last split's sum over them. Fitted to measurements on
-// one MI355X; TM is the number of 16-row tiles. E.g. FP8 output, M = 64: 4096 columns,
-// K = 7168, S = 1 / 2 / 4 / 8: 27.2 / 19.5 / 15.6 / 16.2 us; 8192 columns, K = 2048, S = 1 /
-// 2 / 4: 12.2 / 12.6 / 14.7 us; M = 1, 2048 columns, K = 4096, S = 1 / 2 / 4 / 8: 10.7 / 8.9 /
-// 8.0 / 7.8 us.
+// Estimated times, in units of 0.1 us, fitted to measurements on one MI355X. They choose the
+// K split of the ring kernel and, together with the tile kernel's estimate, the kernel for a
+// product with a fused epilogue.
+//
+// Ring kernel, BM x BN tiles, S splits of `run` pairs of K-blocks each: launch, prologue and
+// epilogue; the pairs; for S > 1 the partials' trip through memory and the last split's sum
+// over them; for more tiles than CUs, further rounds at the rate that L2 leaves to each.
+// bf16 output with residual, gelu:         us, S = 1      2      4      8
+//   M =  64,  4096 columns, K =  7168, 64 x 128 tiles  27.2   19.5   15.6   16.2
+//   M =  64,  8192 columns, K =  2048, 64 x 128        12.2   12.6   14.7
+//   M =   1,  2048 columns, K =  4096, 16 x 128        10.7    8.9    8.0    7.8
+//   M = 256,  4096 columns, K =  7168, 64 x  64        20.5
+//   M = 1008, 4096 columns, K =  7168, 128 x 128       45.1 (64 x 128: 56.5)
 struct RingPlan {
   int64_t S, KS;
+  double time;
 };
 
-RingPlan ring_plan(int64_t tiles, int64_t KB, int tm) {
-  const double pair = tm == 4 ? 8 : tm == 2 ? 6 : 4.5, fixed = tm == 4 ? 25 : tm == 2 ? 18 : 12,
-               each = tm == 4 ? 7.5 : tm == 2 ? 4 : 2.2;
-  const int64_t pairs = (KB + 1) / 2;
-  RingPlan best{1, KB};
-  double least = pair * (double)pairs;
-  for (int64_t S = 2; S <= 8 && S <= pairs && tiles * S <= kCUs; ++S) {
+RingPlan ring_plan(int64_t tiles, int64_t KB, int BM, int BN, int most) {
+  const bool n64 = BN == 64;
+  const double start = BM == 128 ? 75 : 45;
+  const double pair = BM == 128 ? 13 : BM == 64 ? (n64 ? 5.5 : 8.4) : BM == 32 ? (n64 ? 3.6 : 6) : (n64 ? 2.4 : 4);
+  const double fixed = BM >= 64 ? 25 : BM == 32 ? 18 : 12;
+  const double each = BM == 128 ? 15 : BM == 64 ? 7.5 : BM == 32 ? 4 : 2.2;
+  const int64_t pairs = (KB + 1) / 2, rounds = (tiles + kCUs - 1) / kCUs;
+  RingPlan best{1, KB, start + pair * (double)pairs};
+  if (rounds > 1) best.time = start + (double)rounds * 1.2 * pair * (double)pairs + 30 * (double)(rounds - 1);
+  for (int64_t S = 2; S <= most && S <= pairs && tiles * S <= kCUs; ++S) {
     const int64_t run = (pairs + S - 1) / S, used = (pairs + run - 1) / run;
-    const double t = pair * (double)run + fixed + each * (double)used;
-    if (t < least) least = t, best = RingPlan{used, 2 * run};
+    const double t = start + pair * (double)run + fixed + each * (double)used;
+    if (t < best.time) best = RingPlan{used, 2 * run, t};
   }
   return best;
 }
 
+// Tile kernel: 1 us per K-block and round of tiles, the epilogue of each round, and the tail
+// tiles' split (its partial tiles are 128 KB each). M = 512, 4096 columns, K = 7168: 42 us;
+// M = 4096, 7168 columns, K = 2048: 98 us.
+double pipe_time(int64_t M, int64_t N, int64_t KB, int BM, int BN) {
+  const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN);
+  const TailSplit ts = pipe_tail_split(tiles, KB);
+  const double round = 10 * (double)KB + 40;
+  if (ts.parts > 1) return 20 + (double)(ts.full / kCUs) * round + 10 * (double)(KB / ts.parts) + 40 + 170;
+  return 20 + (double)((tiles + kCUs - 1) / kCUs) * round;
+}
+
 template <class Cfg, int EPI>
 dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t stream) {
-  static_assert(Cfg::SMAX >= 8, "ring_plan's splits");
   RingArgs a{};
   a.p = p;
   a.ep = ep;
-  const int64_t tiles = (p.N + Cfg::BN - 1) / Cfg::BN;
-  const RingPlan pl = ring_plan(tiles, p.K / kKBlock, Cfg::BM / 16);
+  a.tiles_m = (int32_t)((p.M + Cfg::BM - 1) / Cfg::BM);
+  const int64_t tiles = a.tiles_m * ((p.N + Cfg::BN - 1) / Cfg::BN);
+  const RingPlan pl = ring_plan(tiles, p.K / kKBlock, Cfg::BM, Cfg::BN, Cfg::SMAX);
   a.S = (int32_t)pl.S;
   a.KS = (int32_t)pl.KS;
   const int64_t grid = tiles * pl.S;
@@ -530,26 +551,38 @@ dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t strea
   return DG_OK;
 }
 
-// The forms by rows and sfA layout. WIDE: 4 waves, 128 columns, B streamed past the caches;
-// otherwise 8 waves (4 for 64 columns and at most 16 rows) and BN columns.
-template <int BN, bool WIDE, int EPI, bool PACKED>
+// The forms by rows and sfA layout. kRing64, kRing128: tiles of 64 or 128 columns and up to 64
+// rows, 8 waves (4 for 64 columns and at most 16 rows). kRing128x128: 128 rows. kRingStream:
+// 128 columns, 4 waves, B streamed past the caches.
+enum RingForm { kRing64, kRing128, kRing128x128, kRingStream };
+
+int ring_bm(RingForm f, int64_t M) { return f == kRing128x128 ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+int ring_bn(RingForm f) { return f == kRing64 ? 64 : 128; }
+
+double ring_time(RingForm f, int64_t M, int64_t N, int64_t KB) {
+  const int BM = ring_bm(f, M), BN = ring_bn(f);
+  return ring_plan((M + BM - 1) / BM * ((N + BN - 1) / BN), KB, BM, BN, f == kRing128x128 ? 2 : 8).time;
+}
+
+template <RingForm F, int EPI, bool PACKED>
 dg_status launch_ring_rows(const Problem& p, const Epilogue& ep, hipStream_t st) {
-  if constexpr (WIDE) {
+  if constexpr (F == kRing128x128) {
+    return launch_ring_as<RingCfg<8, 2, 4, 2, 2, PACKED, false>, EPI>(p, ep, st);
+  } else if constexpr (F == kRingStream) {
     if (p.M <= 16) return launch_ring_as<RingCfg<4, 1, 1, 2, 3, PACKED, true>, EPI>(p, ep, st);
     if (p.M <= 32) return launch_ring_as<RingCfg<4, 1, 2, 2, 3, PACKED, true>, EPI>(p, ep, st);
     return launch_ring_as<RingCfg<4, 1, 4, 2, 3, PACKED, true>, EPI>(p, ep, st);
   } else {
-    constexpr int W1 = BN == 64 ? 4 : 8, TN = BN / 64;
-    if (p.M <= 16) return launch_ring_as<RingCfg<W1, 1, 1, BN / 16 / W1, 3, PACKED, false>, EPI>(p, ep, st);
+    constexpr int W1 = F == kRing64 ? 4 : 8, TN = F == kRing64 ? 1 : 2;
+    if (p.M <= 16) return launch_ring_as<RingCfg<W1, 1, 1, 1, 3, PACKED, false>, EPI>(p, ep, st);
     if (p.M <= 32) return launch_ring_as<RingCfg<8, 2, 1, TN, 3, PACKED, false>, EPI>(p, ep, st);
     return launch_ring_as<RingCfg<8, 2, 2, TN, 3, PACKED, false>, EPI>(p, ep, st);
   }
 }
 
-template <int BN, bool WIDE, int EPI>
+template <RingForm F, int EPI>
 dg_status launch_ring(const Problem& p, const Epilogue& ep, hipStream_t st) {
-  return p.sfa_packed ? launch_ring_rows<BN, WIDE, EPI, true>(p, ep, st)
-                      : launch_ring_rows<BN, WIDE, EPI, false>(p, ep, st);
+  return p.sfa_packed ? launch_ring_rows<F, EPI, true>(p, ep, st) : launch_ring_rows<F, EPI, false>(p, ep, st);
 }
 
 using Stream1x10 = StreamCfg<4, 1, 10>;
@@ -620,12 +653,14 @@ const CfgEntry kTable[] = {
      stream_fits<Stream8w4>},
     {"stream_w2_tn1_d4", launch_stream<Stream2w4>, nullptr, nullptr, 64, 0,
      stream_fits<Stream2w4>},
-    // M <= 64 with a fused epilogue
-    {"ring_n64", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr, launch_ring<64, false, kEpiBf16>},
-    {"ring_n128", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr, nullptr,
-     launch_ring<128, false, kEpiFp8>},
+    // dense with a fused epilogue only
+    {"ring_n64", nullptr, nullptr, nullptr, 0, kPipeMaxKB, nullptr, launch_ring<kRing64, kEpiBf16>},
+    {"ring_n128", nullptr, nullptr, nullptr, 0, kPipeMaxKB, nullptr, launch_ring<kRing128, kEpiBf16>,
+     launch_ring<kRing128, kEpiFp8>},
+    {"ring_m128_n128", nullptr, nullptr, nullptr, 0, kPipeMaxKB, nullptr,
+     launch_ring<kRing128x128, kEpiBf16>, launch_ring<kRing128x128, kEpiFp8>},
     {"ring_n128_wide", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr,
-     launch_ring<128, true, kEpiBf16>, launch_ring<128, true, kEpiFp8>},
+     launch_ring<kRingStream, kEpiBf16>, launch_ring<kRingStream, kEpiFp8>},
 };
 constexpr int kNumCfg = (int)(sizeof(kTable) / sizeof(kTable[0]));
 
@@ -681,17 +716,15 @@ int select_config(int kind, int64_t m, int64_t M, int64_t n, int64_t k, int32_t 
   return find_cfg("pipe128x256");
 }
 
-// From this many bytes on, B is streamed past the caches: the 256 MB MALL cannot be expected
-// to hold it from one use to the next. M = 64, FP8 output, 18432 x 7168 (132 MB): 35.8 us
-// streamed, 40.2 not; 4096 x 7168 (29 MB), read over and over: 17.9 us streamed, 15.6 not.
+// From this many bytes on, with up to 64 rows, B is streamed past the caches: the 256 MB MALL
+// cannot be expected to hold it from one use to the next. M = 64, FP8 output, 18432 x 7168
+// (132 MB): 35.8 us streamed, 40.2 not; 4096 x 7168 (29 MB), read over and over: 17.9 us
+// streamed, 15.6 not.
 constexpr int64_t kStreamB = int64_t(96) << 20;
 
-// Rows from which on the tile kernel's 128x256 tiles serve a product with a fused epilogue.
-constexpr int64_t kRingRows = 64;
-
-// The configuration of the dense GEMM with a fused epilogue; -1 when K is beyond the kernels
-// that have one. FP8 output on M <= 64 needs 128-column workgroups, so that one workgroup
-// holds whole 1x128 blocks of a row; bf16 output gets 64-column ones, twice as many.
+// The configuration of the dense GEMM with a fused epilogue, the one with the least estimated
+// time; -1 when K is beyond the kernels that have one. FP8 output needs 128-column tiles, so
+// that one workgroup holds whole 1x128 blocks of a row.
 int select_epi_config(bool fp8, int64_t M, int64_t N, int64_t K) {
   const auto has = [&](int id) {
     const CfgEntry& c = kTable[id];
@@ -703,11 +736,21 @@ int select_epi_config(bool fp8, int64_t M, int64_t N, int64_t K) {
     const int id = find_cfg(forced);
     if (id >= 0 && has(id)) return id;
   }
-  int id;
-  if (M <= kRingRows)
-    id = find_cfg(N * K >= kStreamB ? "ring_n128_wide" : fp8 ? "ring_n128" : "ring_n64");
-  else
-    id = find_cfg(M <= 128 && (N + 255) / 256 < 8 ? "pipe256x128" : "pipe128x256");
+  const int64_t KB = K / kKBlock;
+  const char* name = "ring_n128_wide";
+  if (M > 64 || N * K < kStreamB) {
+    struct { const char* name; double time; } c[] = {
+        {"ring_n128", ring_time(kRing128, M, N, KB)},
+        {"ring_n64", fp8 ? 1e30 : ring_time(kRing64, M, N, KB)},
+        {"ring_m128_n128", M <= 64 ? 1e30 : ring_time(kRing128x128, M, N, KB)},
+        {"pipe256x128", M <= 64 || M > 128 ? 1e30 : pipe_time(M, N, KB, 256, 128)},
+        {"pipe128x256", M <= 64 ? 1e30 : pipe_time(M, N, KB, 128, 256)}};
+    const auto* best = c;
+    for (const auto& x : c)
+      if (x.time < best->time) best = &x;
+    name = best->name;
+  }
+  const int id = find_cfg(name);
   return has(id) ? id : -1;
 }
 

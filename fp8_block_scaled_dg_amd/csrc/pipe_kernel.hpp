@@ -774,8 +774,8 @@ __device__ __forceinline__ void pipe_store(const Problem& p, const TileView& v, 
 // through its 4 KB of LDS stage 2, 16 rows at a time (256 bytes a row, 16-byte chunk q of
 // row r at q ^ r), and reads it back with 8 lanes per row, 8 columns each: a lane's columns
 // are the same in all rows, so it loads its bias once, and residual, pre and C move as whole
-// 128-byte row segments. The residual of a 16-row pass is loaded before the pass's LDS
-// traffic. The activation sits in a loop that is not unrolled: it costs code for 8 values,
+// 128-byte row segments. All of the residual is loaded before the first pass, one wait for
+// memory per tile. The activation sits in a loop that is not unrolled: it costs code for 8 values,
 // not for 64.
 // kEpiFp8: a row's 1x128 block is shared by two waves (wn and wn ^ 1), which hold its two
 // 64-column halves. Each keeps its 64 values per lane, the row maxima meet in pipe_rmax
@@ -803,17 +803,18 @@ __device__ __forceinline__ void pipe_store_epi(const Problem& p, const TileView&
   for (int i = 0; i < 8; ++i) b[i] = 0.f;
   if (col_ok) epi_bias8(ep, col, b);
   float keep[EPI == kEpiFp8 ? 8 : 1][8];
+  v4u res[EPI == kEpiBf16 ? 8 : 1];
+  if (EPI == kEpiBf16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t row = row0 + 8 * k;
+      res[k] = v4u{0, 0, 0, 0};
+      if (ep.residual && col_ok && row < p.M)
+        res[k] = __builtin_nontemporal_load((const v4u*)(ep.residual + row * N + col));
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 4; ++h) {  // 16-row passes
-    v4u res[2] = {v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}};
-    if (EPI == kEpiBf16 && ep.residual) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int64_t row = row0 + 16 * h + 8 * k;
-        if (col_ok && row < p.M)
-          res[k] = __builtin_nontemporal_load((const v4u*)(ep.residual + row * N + col));
-      }
-    }
     if ((r32 >> 4) == (h & 1)) {
       const int r = r32 & 15;
 #pragma unroll
@@ -846,7 +847,7 @@ __device__ __forceinline__ void pipe_store_epi(const Problem& p, const TileView&
       const int64_t off = row * N + col;
       if (ok) epi_act8(ep, b, off, x[k]);
       if (EPI == kEpiBf16) {
-        if (ok) epi_store8(res[k], v.C, off, x[k]);
+        if (ok) epi_store8(res[2 * h + k], v.C, off, x[k]);
       } else {
         float m = 0.f;
 #pragma unroll

@@ -1,9 +1,11 @@
-// ring_kernel.hpp -- block-scaled FP8 GEMM for M <= 64 with a fused epilogue, for units of
-// many K-blocks, gfx950.
+// ring_kernel.hpp -- block-scaled FP8 GEMM with a fused epilogue for few rows or few tiles,
+// gfx950: tiles of up to 64 (or 128) x 64 or 128, a quarter or an eighth of the tile kernel's,
+// so that products of a few hundred rows still give every CU a tile without splitting K, or
+// with partial tiles of 16 or 32 KB instead of 128.
 //
-// Memory-bound: every byte of B meets at most 64 rows of A, so the kernel has to keep enough
-// bytes of B in flight on every CU, and to ask for them in the right pieces. A workgroup (4
-// waves) takes BN columns and a run of consecutive K-blocks. It moves A and B by LDS DMA,
+// Memory-bound: with up to 64 rows every byte of B meets few rows of A, so the kernel has to
+// keep enough bytes of B in flight on every CU, and to ask for them in the right pieces. A
+// workgroup (4 or 8 waves) takes a tile and a run of consecutive K-blocks. It moves A and B by LDS DMA,
 // two K-blocks at a time: 256 contiguous bytes of every row. (Reading B [18432][7168] alone,
 // 128 bytes of each of 128 rows per step, took 41 us; 256 bytes, 26 us, and the rate that one
 // CU reaches grew with it: 32 workgroups on [4096][7168], 24.7 against 14.0 us.) D stages of
@@ -26,8 +28,8 @@
 // length reads 128 bytes per row past its end (the next row's, or zeros past the last) and
 // does not compute them.
 //
-// sfA: each wave brings 16 rows' values of both blocks by one 4-byte DMA per lane. TM: 16-row
-// tiles that hold rows (1, 2 or 4). Rows past M and N read as zero (the buffer resources end
+// sfA: each wave brings 16 rows' values of both blocks by one 4-byte DMA per lane (waves past
+// the tile's rows repeat others'). Rows past M and N read as zero (the buffer resources end
 // there) and are never stored.
 //
 // S > 1 K splits: fp32 partials and an arrival count per column tile, the last split to
@@ -36,6 +38,7 @@
 
 #include "epilogue.hpp"
 #include "gemm_kernel.hpp"
+#include "pipe_kernel.hpp"
 
 namespace dg {
 
@@ -51,10 +54,12 @@ struct RingCfg {
   static constexpr int A_DMA = A_ROWS / 4 / W, B_DMA = BN / 4 / W;  // 1 KB DMAs per wave and step
   static constexpr int OPS = 1 + A_DMA + B_DMA;
   static constexpr int OFF_B = A_ROWS * ROW, OFF_S = OFF_B + BN * ROW;
-  static constexpr int STAGE = OFF_S + 4 * 256;
-  static constexpr int SMAX = 8;
+  static constexpr int SROWS = BM <= 64 ? 4 : 8;  // 16-row groups whose scales are staged
+  static constexpr int STAGE = OFF_S + SROWS * 256;
+  static constexpr int SMAX = TM * TN <= 4 ? 8 : 2;  // splits whose partials fit the registers
   static constexpr int ROWS = BM < 32 ? BM : 32;  // rows per pass of the epilogue
-  static_assert(BM <= 64 && B_DMA >= 1 && W % 4 == 0, "DMA split");
+  static_assert(SROWS <= W && BM <= 16 * SROWS, "scale rows");
+  static_assert(BM <= 128 && B_DMA >= 1 && W % 4 == 0, "DMA split");
   static_assert(ROWS * kEpiPitch<BN> * 4 <= OFF_S, "a pass of the fp32 tile fits a stage");
   static_assert((D - 1) * OPS < 64, "vmcnt range");
 };
@@ -63,7 +68,8 @@ struct RingArgs {
   Problem p;
   float* ws;           // [tiles][S][BM * BN] fp32 partials (S > 1)
   uint32_t* counters;  // [tiles], zero between calls
-  int32_t S, KS;       // K splits, K-blocks per split (the last may have fewer)
+  int32_t S, KS;       // K splits, K-blocks per split (even; the last may have fewer)
+  int32_t tiles_m;     // row tiles
   Epilogue ep;
 };
 
@@ -89,7 +95,7 @@ __device__ __forceinline__ void ring_issue(const RingSrc<Cfg>& src, int t) {
   constexpr int kPolicyB = Cfg::STREAM_B ? 2 : 0;  // 2: non-temporal
   uint8_t* st = ring_stage<Cfg::STAGE, T>;
   const int kb = src.kb0 + 2 * t;  // even: in the packed form both blocks lie in one word
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.s, (lds_ptr)(st + Cfg::OFF_S + (src.wave & 3) * 256), 4, src.s_off,
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.s, (lds_ptr)(st + Cfg::OFF_S + (src.wave & (Cfg::SROWS - 1)) * 256), 4, src.s_off,
                                            Cfg::PACKED ? kb & ~3 : kb * 4, 0, 0);
 #pragma unroll
   for (int q = 0; q < Cfg::A_DMA; ++q)
@@ -193,9 +199,14 @@ __global__ void __launch_bounds__(Cfg::NT) ring_kernel(RingArgs args) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, l16 = lane & 15;
   const int64_t N = p.N, K = p.K;
-  const int M = (int)p.M, KB = (int)(K / kKBlock), S = args.S;
-  const int tile = blockIdx.x / S, split = blockIdx.x - tile * S;
-  const int64_t n0 = (int64_t)tile * BN;
+  const int KB = (int)(K / kKBlock), S = args.S;
+  // units in the order column tile, split, row tile (fastest); each XCD takes a contiguous
+  // range of it, so that the row tiles that read the same part of B share its L2
+  const int unit = xcd_tile_order(blockIdx.x, gridDim.x);
+  const int mt = unit % args.tiles_m, rest = unit / args.tiles_m;
+  const int split = rest % S, nt = rest / S, tile = nt * args.tiles_m + mt;
+  const int64_t n0 = (int64_t)nt * BN, m0 = (int64_t)mt * Cfg::BM;
+  const int M = (int)(p.M - m0 < Cfg::BM ? p.M - m0 : Cfg::BM);  // rows of this tile
   const int kb0 = split * args.KS;
   const int ks = min(args.KS, KB - kb0);  // >= 1 (host guarantees)
 
@@ -205,12 +216,14 @@ __global__ void __launch_bounds__(Cfg::NT) ring_kernel(RingArgs args) {
   {
     const int64_t rb = sfa_row_bytes(KB, Cfg::PACKED);
     const int64_t b_rows = N - n0 < BN ? N - n0 : BN, skip = (int64_t)kb0 * kKBlock;
-    src.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.A + skip), 0, (int)(M * K - skip), 0x00020000);
+    src.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.A + m0 * K + skip), 0,
+                                              (int)(M * K - skip), 0x00020000);
     src.b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.B + n0 * K + skip), 0,
                                               (int)(b_rows * K - skip), 0x00020000);
-    src.s = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.sfA), 0, (int)(M * rb), 0x00020000);
+    src.s = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.sfA + m0 * rb), 0, (int)(M * rb),
+                                              0x00020000);
     // lane (h, row): block h of the pair (the packed form: the word both lie in)
-    src.s_off = (uint32_t)((wave & 3) * 16 + l16) * (uint32_t)rb + (Cfg::PACKED ? 0 : 4 * (g & 1));
+    src.s_off = (uint32_t)((wave & (Cfg::SROWS - 1)) * 16 + l16) * (uint32_t)rb + (Cfg::PACKED ? 0 : 4 * (g & 1));
 #pragma unroll
     for (int q = 0; q < Cfg::A_DMA; ++q) {
       const int r = (wave * Cfg::A_DMA + q) * 4 + (lane >> 4);
@@ -301,7 +314,7 @@ __global__ void __launch_bounds__(Cfg::NT) ring_kernel(RingArgs args) {
         *(v4f*)(out + (row + l16) * kEpiPitch<BN> + (wn * TN + j) * 16 + 4 * g) = acc[i][j];
     }
     __syncthreads();
-    epi_finish_tile<BN, Cfg::NT, EPI, ROWS>(p, n0, out, args.ep, ROWS * h);
+    epi_finish_tile<BN, Cfg::NT, EPI, ROWS>(p, n0, out, args.ep, (int)m0 + ROWS * h);
   }
 }
 

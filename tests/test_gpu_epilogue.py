@@ -187,12 +187,11 @@ def test_row_counts_and_run_lengths(monkeypatch, config, M, N, KB):
     packed = (M + KB) % 2 == 0
     A, B, sfA, sfB, r = operands(M, N, 128 * KB, M + N + KB)
     a, b, sa, sb = gu.codes(A), gu.codes(B), pack(sfA) if packed else gu.dev(sfA), gu.dev(sfB)
-    if config != "ring_n128":
-        out = gu.Guarded((M, N), 5)
-        gu.announce(f"{config} M={M} N={N} KB={KB}")
-        dg().fp8_gemm_nt_bias_act(a, b, out.out, sa, sb)
-        torch.cuda.synchronize()
-        assert out.guards_intact() and np.array_equal(out.result(), oracle.bf16_rne(r))
+    out = gu.Guarded((M, N), 5)
+    gu.announce(f"{config} M={M} N={N} KB={KB}")
+    dg().fp8_gemm_nt_bias_act(a, b, out.out, sa, sb)
+    torch.cuda.synchronize()
+    assert out.guards_intact() and np.array_equal(out.result(), oracle.bf16_rne(r))
     if fp8:
         out = Fp8Out(M, N, not packed)
         gu.announce(f"{config} FP8 M={M} N={N} KB={KB}")
@@ -202,8 +201,35 @@ def test_row_counts_and_run_lengths(monkeypatch, config, M, N, KB):
         assert np.array_equal(rs, sf) and np.array_equal(rc, codes)
 
 
+@pytest.mark.parametrize("config", ["ring_n64", "ring_n128", "ring_m128_n128", "pipe128x256", "pipe256x128"])
+@pytest.mark.parametrize("M,N,KB", [(65, 128, 1), (127, 384, 4), (129, 256, 5), (200, 640, 12), (300, 1040, 7),
+                                    (257, 128, 40), (700, 2176, 3)])
+def test_row_tiles(monkeypatch, config, M, N, KB):
+    """Several row tiles, a ragged last one, with and without split K, on each kernel that
+    the choice by estimated time may take."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", config)
+    packed = (M + KB) % 2 == 0
+    A, B, sfA, sfB, r = operands(M, N, 128 * KB, M + N + KB)
+    a, b, sa, sb = gu.codes(A), gu.codes(B), pack(sfA) if packed else gu.dev(sfA), gu.dev(sfB)
+    residual = small_values(23, (M, N), BF)
+    out, pre = gu.Guarded((M, N), 5), gu.Guarded((M, N), 6)
+    gu.announce(f"{config} M={M} N={N} KB={KB}")
+    dg().fp8_gemm_nt_bias_act(a, b, out.out, sa, sb, residual=residual.cuda(), pre=pre.out)
+    torch.cuda.synchronize()
+    assert out.guards_intact() and np.array_equal(out.result(), oracle.bf16_rne(r + residual.double().numpy()))
+    assert pre.guards_intact() and np.array_equal(pre.result(), oracle.bf16_rne(r))
+    if N % 128 == 0 and config != "ring_n64":
+        fp8 = Fp8Out(M, N, not packed)
+        gu.announce(f"{config} FP8 M={M} N={N} KB={KB}")
+        dg().fp8_gemm_nt_bias_act_fp8(a, b, sa, sb, codes=fp8.codes, sf=fp8.sf)
+        codes, sf = fp8.result()
+        rc, rs = oracle.quantize_blocks(r.astype(np.float32), 1, 128)
+        assert np.array_equal(rs, sf) and np.array_equal(rc, codes)
+
+
 @pytest.mark.parametrize("M,N,K", [(130, 2112, 2048), (1000, 1024, 512)])
-def test_plain_call_and_no_epilogue_agree(M, N, K):
+def test_plain_call_and_no_epilogue_agree(monkeypatch, M, N, K):
+    monkeypatch.setenv("DG_FORCE_CONFIG", "pipe128x256")
     # nothing to add: the same bits as the plain call, whose kernel this is
     rng = np.random.default_rng(13)
     A, sfA = oracle.quantize_blocks(rng.normal(size=(M, K)).astype(np.float32), 1, 128)
