@@ -373,6 +373,7 @@ def quantize_fp8_1x128(x, codes=None, sf=None):
 
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_get_device = torch._C._cuda_getDevice
 
 
 def _float_type(t: torch.Tensor, name: str) -> int:
@@ -389,23 +390,51 @@ def _act(activation) -> int:
     return code
 
 
-def _fp8_outputs(M: int, N: int, codes, sf, ue8m0: bool, dev):
-    """(codes, sf, packed?) of an FP8 output [M, N]: new tensors where none is passed. The
-    dtype of a passed sf (float32, or int32 for packed UE8M0) says its form."""
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, shape, x: torch.Tensor, index: int) -> int:
+    """t's address, once it has this dtype and shape, is contiguous and lies on the GPU
+    `index` of x (the test of _need in its quickest form; a call checks up to seven tensors)."""
+    if (t.dtype is not dtype or t.get_device() != index or t.shape != shape
+            or not t.is_contiguous()):
+        _need(t, name, dtype, tuple(shape), x.device)
+    return t.data_ptr()
+
+
+def _first(x: torch.Tensor, name: str) -> int:
+    """The GPU index of a call's first tensor, which has to be contiguous."""
+    index = x.get_device()
+    if index < 0 or not x.is_contiguous():
+        _dev(x, name, x.device)
+    return index
+
+
+def _launch(index: int, fn, *args) -> None:
+    """_run for a GPU index; a call's tensors exist, so HIP is initialised."""
+    if _get_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        raise DGError(status)
+
+
+def _fp8_outputs(M: int, N: int, codes, sf, ue8m0: bool, x: torch.Tensor, index: int):
+    """(codes, codes pointer, sf, sf pointer, packed?) of an FP8 output [M, N]: new tensors
+    where none is passed. The dtype of a passed sf (float32, or int32 for packed UE8M0) says
+    its form."""
     if codes is None:
-        codes = torch.empty((M, N), dtype=torch.float8_e4m3fn, device=dev)
+        codes = torch.empty((M, N), dtype=torch.float8_e4m3fn, device=x.device)
+        codes_ptr = codes.data_ptr()
     else:
         _fp8(codes, "codes")
-        _need(codes, "codes", codes.dtype, (M, N), dev)
+        codes_ptr = _ptr(codes, "codes", codes.dtype, (M, N), x, index)
     if sf is None:
-        sf = (torch.empty((M, (N // BLOCK + 3) // 4), dtype=torch.int32, device=dev) if ue8m0 else
-              torch.empty((M, N // BLOCK), dtype=torch.float32, device=dev))
-        return codes, sf, ue8m0
-    if sf.dtype == torch.int32:
-        _need(sf, "sf", torch.int32, (M, (N // BLOCK + 3) // 4), dev)
-        return codes, sf, True
-    _need(sf, "sf", torch.float32, (M, N // BLOCK), dev)
-    return codes, sf, False
+        sf = (torch.empty((M, (N // BLOCK + 3) // 4), dtype=torch.int32, device=x.device) if ue8m0
+              else torch.empty((M, N // BLOCK), dtype=torch.float32, device=x.device))
+        return codes, codes_ptr, sf, sf.data_ptr(), ue8m0
+    if sf.dtype is torch.int32:
+        return codes, codes_ptr, sf, _ptr(sf, "sf", torch.int32, (M, (N // BLOCK + 3) // 4), x, index), True
+    return codes, codes_ptr, sf, _ptr(sf, "sf", torch.float32, (M, N // BLOCK), x, index), False
 
 
 def rmsnorm_fp8_1x128(x, weight, eps=1e-6, residual=None, h=None, rstd=None, codes=None, sf=None,
@@ -417,22 +446,16 @@ def rmsnorm_fp8_1x128(x, weight, eps=1e-6, residual=None, h=None, rstd=None, cod
     rstd (fp32 [M]) 1 / rms; rmsnorm_backward takes both."""
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
-    dtype = _float_type(x, "x")
-    M, K = x.shape
-    dev = x.device
-    _dev(x, "x", dev)
-    w_dtype = _float_type(weight, "weight")
-    _need(weight, "weight", weight.dtype, (K,), dev)
-    if residual is not None:
-        _need(residual, "residual", x.dtype, (M, K), dev)
-    if h is not None:
-        _need(h, "h", x.dtype, (M, K), dev)
-    if rstd is not None:
-        _need(rstd, "rstd", torch.float32, (M,), dev)
-    codes, sf, packed = _fp8_outputs(M, K, codes, sf, ue8m0, dev)
-    _run(dev, lib.dg_rmsnorm_fp8_1x128, x.data_ptr(), residual.data_ptr() if residual is not None else None,
-         dtype, weight.data_ptr(), w_dtype, eps, h.data_ptr() if h is not None else None,
-         rstd.data_ptr() if rstd is not None else None, codes.data_ptr(), sf.data_ptr(), packed, M, K)
+    dtype, w_dtype = _float_type(x, "x"), _float_type(weight, "weight")
+    M, K = shape = x.shape
+    dev = _first(x, "x")
+    w = _ptr(weight, "weight", weight.dtype, (K,), x, dev)
+    r = None if residual is None else _ptr(residual, "residual", x.dtype, shape, x, dev)
+    hp = None if h is None else _ptr(h, "h", x.dtype, shape, x, dev)
+    rs = None if rstd is None else _ptr(rstd, "rstd", torch.float32, (M,), x, dev)
+    codes, cp, sf, sp, packed = _fp8_outputs(M, K, codes, sf, ue8m0, x, dev)
+    _launch(dev, lib.dg_rmsnorm_fp8_1x128, x.data_ptr(), r, dtype, w, w_dtype, eps, hp, rs, cp, sp,
+            packed, M, K)
     return codes, sf
 
 
@@ -443,53 +466,44 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None):
     of x and of residual alike, and may be dy, dh or h itself."""
     if h.dim() != 2:
         raise ValueError("h must be [M, K]")
-    dtype = _float_type(h, "h")
-    M, K = h.shape
-    dev = h.device
-    _dev(h, "h", dev)
-    _need(dy, "dy", h.dtype, (M, K), dev)
-    w_dtype = _float_type(weight, "weight")
-    _need(weight, "weight", weight.dtype, (K,), dev)
-    _need(rstd, "rstd", torch.float32, (M,), dev)
-    if dh is not None:
-        _need(dh, "dh", h.dtype, (M, K), dev)
+    dtype, w_dtype = _float_type(h, "h"), _float_type(weight, "weight")
+    M, K = shape = h.shape
+    dev = _first(h, "h")
+    g = _ptr(dy, "dy", h.dtype, shape, h, dev)
+    w = _ptr(weight, "weight", weight.dtype, (K,), h, dev)
+    rs = _ptr(rstd, "rstd", torch.float32, (M,), h, dev)
+    r = None if dh is None else _ptr(dh, "dh", h.dtype, shape, h, dev)
     if dx is None:
         dx = torch.empty_like(h)
-    else:
-        _need(dx, "dx", h.dtype, (M, K), dev)
     if dweight is None:
-        dweight = torch.empty((K,), dtype=torch.float32, device=dev)
-    else:
-        _need(dweight, "dweight", torch.float32, (K,), dev)
-    _run(dev, lib.dg_rmsnorm_backward, dy.data_ptr(), dh.data_ptr() if dh is not None else None,
-         h.data_ptr(), dtype, weight.data_ptr(), w_dtype, rstd.data_ptr(), dx.data_ptr(),
-         dweight.data_ptr(), M, K)
+        dweight = torch.empty((K,), dtype=torch.float32, device=h.device)
+    _launch(dev, lib.dg_rmsnorm_backward, g, r, h.data_ptr(), dtype, w, w_dtype, rs,
+            _ptr(dx, "dx", h.dtype, shape, h, dev), _ptr(dweight, "dweight", torch.float32, (K,), h, dev),
+            M, K)
     return dx, dweight
 
 
 def _bias_act_operands(a, b, a_sf, b_sf, bias, pre):
-    """Checks what the two epilogue GEMMs share: (M, N, K, device, packed a_sf?, bias pointer,
-    bias dtype, pre pointer)."""
+    """Checks what the two epilogue GEMMs share: (M, N, K, GPU index, a, b, a_sf, packed?,
+    b_sf, bias, bias dtype, pre), tensors as addresses."""
     _fp8(a, "a"), _fp8(b, "b")
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b must be 2-D")
     M, K = a.shape
     N = b.shape[0]
-    dev = a.device
-    _dev(a, "a", dev)
-    _need(b, "b", b.dtype, (N, K), dev)
-    packed = _a_sf_layout(a_sf, (M,), K, dev)
-    _need(b_sf, "b_sf", torch.float32, ((N + BLOCK - 1) // BLOCK, K // BLOCK), dev)
+    dev = _first(a, "a")
+    bp = _ptr(b, "b", b.dtype, (N, K), a, dev)
+    KB = K // BLOCK
+    packed = a_sf.dtype is torch.int32
+    ap = (_ptr(a_sf, "a_sf", torch.int32, (M, (KB + 3) // 4), a, dev) if packed
+          else _ptr(a_sf, "a_sf", torch.float32, (M, KB), a, dev))
+    sp = _ptr(b_sf, "b_sf", torch.float32, ((N + BLOCK - 1) // BLOCK, KB), a, dev)
     bias_ptr, bias_dtype = None, 0
     if bias is not None:
         bias_dtype = _float_type(bias, "bias")
-        _need(bias, "bias", bias.dtype, (N,), dev)
-        bias_ptr = bias.data_ptr()
-    pre_ptr = None
-    if pre is not None:
-        _need(pre, "pre", torch.bfloat16, (M, N), dev)
-        pre_ptr = pre.data_ptr()
-    return M, N, K, dev, packed, bias_ptr, bias_dtype, pre_ptr
+        bias_ptr = _ptr(bias, "bias", bias.dtype, (N,), a, dev)
+    pre_ptr = None if pre is None else _ptr(pre, "pre", torch.bfloat16, (M, N), a, dev)
+    return M, N, K, dev, a.data_ptr(), bp, ap, packed, sp, bias_ptr, bias_dtype, pre_ptr
 
 
 def fp8_gemm_nt_bias_act(a, b, c, a_sf, b_sf, bias=None, activation=None, residual=None,
@@ -498,13 +512,12 @@ def fp8_gemm_nt_bias_act(a, b, c, a_sf, b_sf, bias=None, activation=None, residu
     place. a, b and the scales as for fp8_gemm_nt; bias [N] float32 or bfloat16; activation
     None, "relu", "silu", "gelu" or "gelu_tanh"; residual [M, N] bf16 (c itself is allowed);
     pre, when passed, receives a x b^T + bias (bf16 [M, N], for bias_act_backward_fp8)."""
-    M, N, K, dev, packed, bias_ptr, bias_dtype, pre_ptr = _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
-    _need(c, "c", torch.bfloat16, (M, N), dev)
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (M, N), dev)
-    _run(dev, lib.dg_fp8_gemm_nt_bias_act, a.data_ptr(), b.data_ptr(), c.data_ptr(), a_sf.data_ptr(),
-         packed, b_sf.data_ptr(), bias_ptr, bias_dtype, _act(activation),
-         residual.data_ptr() if residual is not None else None, pre_ptr, M, N, K)
+    M, N, K, dev, ap, bp, sa, packed, sb, bias_ptr, bias_dtype, pre_ptr = \
+        _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
+    cp = _ptr(c, "c", torch.bfloat16, (M, N), a, dev)
+    r = None if residual is None else _ptr(residual, "residual", torch.bfloat16, (M, N), a, dev)
+    _launch(dev, lib.dg_fp8_gemm_nt_bias_act, ap, bp, cp, sa, packed, sb, bias_ptr, bias_dtype,
+            _act(activation), r, pre_ptr, M, N, K)
 
 
 def fp8_gemm_nt_bias_act_fp8(a, b, a_sf, b_sf, bias=None, activation=None, pre=None, codes=None,
@@ -512,11 +525,11 @@ def fp8_gemm_nt_bias_act_fp8(a, b, a_sf, b_sf, bias=None, activation=None, pre=N
     """activation(a x b^T + bias) quantized per 1x128 block: returns (codes [M, N] e4m3fn,
     sf), the next GEMM's a and a_sf (sf as in rmsnorm_fp8_1x128). N % 128 == 0; the other
     arguments as for fp8_gemm_nt_bias_act."""
-    M, N, K, dev, packed, bias_ptr, bias_dtype, pre_ptr = _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
-    codes, sf, sf_packed = _fp8_outputs(M, N, codes, sf, ue8m0, dev)
-    _run(dev, lib.dg_fp8_gemm_nt_bias_act_fp8, a.data_ptr(), b.data_ptr(), codes.data_ptr(),
-         sf.data_ptr(), sf_packed, a_sf.data_ptr(), packed, b_sf.data_ptr(), bias_ptr, bias_dtype,
-         _act(activation), pre_ptr, M, N, K)
+    M, N, K, dev, ap, bp, sa, packed, sb, bias_ptr, bias_dtype, pre_ptr = \
+        _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
+    codes, cp, sf, sp, sf_packed = _fp8_outputs(M, N, codes, sf, ue8m0, a, dev)
+    _launch(dev, lib.dg_fp8_gemm_nt_bias_act_fp8, ap, bp, cp, sp, sf_packed, sa, packed, sb, bias_ptr,
+            bias_dtype, _act(activation), pre_ptr, M, N, K)
     return codes, sf
 
 
@@ -529,21 +542,16 @@ def bias_act_backward_fp8(dc, pre=None, activation=None, codes=None, sf=None, db
     b_sf.t().contiguous()) with the forward call's b."""
     if dc.dim() != 2:
         raise ValueError("dc must be [M, N]")
-    M, N = dc.shape
-    dev = dc.device
-    _dev(dc, "dc", dev)
-    _need(dc, "dc", torch.bfloat16, (M, N), dev)
+    M, N = shape = dc.shape
+    dev = _first(dc, "dc")
+    d = _ptr(dc, "dc", torch.bfloat16, shape, dc, dev)
     act = _act(activation)
-    if pre is not None:
-        _need(pre, "pre", torch.bfloat16, (M, N), dev)
-    codes, sf, packed = _fp8_outputs(M, N, codes, sf, ue8m0, dev)
-    if dbias is not None:
-        _need(dbias, "dbias", torch.float32, (N,), dev)
-    elif need_dbias:
-        dbias = torch.empty((N,), dtype=torch.float32, device=dev)
-    _run(dev, lib.dg_bias_act_backward_fp8, dc.data_ptr(), pre.data_ptr() if pre is not None else None,
-         act, codes.data_ptr(), sf.data_ptr(), packed, dbias.data_ptr() if dbias is not None else None,
-         M, N)
+    z = None if pre is None else _ptr(pre, "pre", torch.bfloat16, shape, dc, dev)
+    codes, cp, sf, sp, packed = _fp8_outputs(M, N, codes, sf, ue8m0, dc, dev)
+    if dbias is None and need_dbias:
+        dbias = torch.empty((N,), dtype=torch.float32, device=dc.device)
+    db = None if dbias is None else _ptr(dbias, "dbias", torch.float32, (N,), dc, dev)
+    _launch(dev, lib.dg_bias_act_backward_fp8, d, z, act, cp, sp, packed, db, M, N)
     return codes, sf, dbias
 
 

@@ -1275,6 +1275,13 @@ int norm_threads(int64_t K) {
   return (int)((t + 63) / 64 * 64);
 }
 
+// Up to this many rows the backward kernels sum columns in the same launch, reading their
+// inputs a second time; for the activation's, whose values are also computed twice, up to
+// this many values. Back to back calls, us, one launch against two (3 us of host time each):
+// norm bf16 64 x 7168 7.7, 10.3; 256 x 7168 7.6, 11.4; 512 x 2048 fp32 10.0, 9.8; gelu
+// 64 x 18432 7.0, 9.7; 130 x 18432 11.3, 9.7; 256 x 2048 7.1, 9.9.
+constexpr int64_t kDirectRows = 256, kDirectActValues = 3 << 19;
+
 // Workgroups for `rows` steps of work, at most `most`, evened out so that every workgroup
 // takes the same number of steps or one fewer (bf16 4096 x 7168 on 512 workgroups, 8 rows
 // each: 34.5 us; on 768, 5 or 6 each: 39.1).
@@ -1413,19 +1420,22 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
   int64_t R = nt < 512 ? 512 / nt : 1;
   if (R > (M + kCUs - 1) / kCUs) R = (M + kCUs - 1) / kCUs;
   const int64_t G = even_grid((M + R - 1) / R, kCUs);
+  const bool direct = M <= kDirectRows;
   float* part = nullptr;
-  uint32_t* counters = nullptr;
-  s = get_workspace(st, (size_t)(G * K) * sizeof(float), 0, &part, &counters);
-  if (s != DG_OK) return s;
-  NormBwdArgs a{dy, dh, h, weight, rstd, dx, part, M, (int32_t)K, (int32_t)R};
+  if (!direct) {
+    uint32_t* counters = nullptr;
+    s = get_workspace(st, (size_t)(G * K) * sizeof(float), 0, &part, &counters);
+    if (s != DG_OK) return s;
+  }
+  NormBwdArgs a{dy, dh, h, weight, rstd, dx, part, dweight, M, (int32_t)K, (int32_t)R, (int32_t)G};
+  const unsigned grid = (unsigned)(G + (direct ? K / 64 : 0));
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c, auto n) {
     constexpr bool ahead = n.value <= 512;
     hipLaunchKernelGGL((rmsnorm_backward_kernel<xb.value, wb.value, c.value, n.value, ahead>),
-                       dim3((unsigned)G), dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float),
-                       st, a);
+                       dim3(grid), dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
   });
   s = launched("rmsnorm_backward_kernel");
-  return s == DG_OK ? launch_column_sum(part, dweight, G, K, st) : s;
+  return s == DG_OK && !direct ? launch_column_sum(part, dweight, G, K, st) : s;
 }
 
 dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t activation, void* codes,
@@ -1450,18 +1460,20 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
   if (groups > (M + 3) / 4) groups = (M + 3) / 4;
   const int64_t rows = ((M + groups - 1) / groups + 3) / 4 * 4;
   groups = (M + rows - 1) / rows;
+  const bool direct = dbias && M <= kDirectRows && M * N <= kDirectActValues, sum = dbias && !direct;
   float* part = nullptr;
-  uint32_t* counters = nullptr;
-  if (dbias) {
+  if (sum) {
+    uint32_t* counters = nullptr;
     s = get_workspace(st, (size_t)(groups * N) * sizeof(float), 0, &part, &counters);
     if (s != DG_OK) return s;
   }
   ActBwdArgs a{(const uint16_t*)dc, (const uint16_t*)pre, (uint8_t*)codes,
-               ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)}, part, M, rows,
-               (int32_t)N, activation, (int32_t)strips};
-  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)(strips * groups)), dim3(256), 0, st, a);
+               ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)}, part, dbias, M, rows,
+               (int32_t)N, activation, (int32_t)strips, (int32_t)groups};
+  const unsigned grid = (unsigned)(strips * groups + (direct ? N / 64 : 0));
+  hipLaunchKernelGGL(act_backward_kernel, dim3(grid), dim3(256), 0, st, a);
   s = launched("act_backward_kernel");
-  return s == DG_OK && dbias ? launch_column_sum(part, dbias, groups, N, st) : s;
+  return s == DG_OK && sum ? launch_column_sum(part, dbias, groups, N, st) : s;
 }
 
 }  // extern "C"

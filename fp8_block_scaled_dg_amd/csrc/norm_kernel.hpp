@@ -15,7 +15,9 @@
 //
 // Column sums (dweight, dbias): every workgroup sums its own rows in registers and writes
 // one fp32 row of partials; column_sum_kernel adds the partials in a fixed order, so the
-// results do not depend on scheduling.
+// results do not depend on scheduling. With few rows the second launch costs more than
+// reading them twice: then the launch holds a second kind of workgroup, which sums 64 columns
+// over all rows (direct_column_sums) and writes the result itself.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -218,6 +220,39 @@ __device__ __forceinline__ void lds_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Sums 64 columns (from col0) over all rows, for workgroups of blockDim.x threads (a multiple
+// of 64, at most NT): groups of 64 / P lanes of P values take rows r, r + groups, ...; add(m,
+// col, v) adds row m's values at columns col .. col + P - 1 to v. The groups' sums are added
+// in order through LDS.
+template <int P, int NT, class F>
+__device__ __forceinline__ void direct_column_sums(int64_t M, int col0, float* out, F add) {
+  constexpr int L = 64 / P;
+  __shared__ float sums[NT / L][64];
+  const int groups = blockDim.x / L, r = threadIdx.x / L, c = (threadIdx.x % L) * P;
+  float v[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = 0.f;
+  for (int64_t m = r; m < M; m += groups) add(m, col0 + c, v);
+#pragma unroll
+  for (int i = 0; i < P; ++i) sums[r][c + i] = v[i];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float s = 0.f;
+    for (int i = 0; i < groups; ++i) s += sums[i][threadIdx.x];
+    out[col0 + threadIdx.x] = s;
+  }
+}
+
+// P consecutive values of a bf16 (P = 8) or fp32 (P = 4) array, 16 bytes.
+template <bool BF16>
+__device__ __forceinline__ void load_piece(const void* src, int64_t idx, float (&v)[Pieces<BF16>::P]) {
+  const quant_v4u u = *(BF16 ? (const quant_v4u*)((const uint16_t*)src + idx)
+                             : (const quant_v4u*)((const float*)src + idx));
+#pragma unroll
+  for (int i = 0; i < Pieces<BF16>::P; ++i)
+    v[i] = __uint_as_float(!BF16 ? u[i & 3] : i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+}
+
 // Sum of v over a row's `waves` waves, of which `wave` is this one, the same in every
 // thread, added in a fixed order. buf: one float per wave of the row, not written again
 // before another barrier has passed (two buffers in turn).
@@ -320,10 +355,12 @@ struct NormBwdArgs {
   const void* w;
   const float* rstd;
   void* dx;
-  float* part;     // [gridDim.x][K] partial dweight
+  float* part;     // [groups][K] partial dweight; NULL: workgroups from `groups` on sum it
+  float* dweight;  // part == NULL: the sums
   int64_t M;
   int32_t K;
   int32_t teams;   // rows that a workgroup works on side by side
+  int32_t groups;  // workgroups that take rows
 };
 
 // A workgroup is `teams` teams of threads, each on a row of its own (the columns of
@@ -338,6 +375,19 @@ __global__ void __launch_bounds__(NT) rmsnorm_backward_kernel(NormBwdArgs a) {
   __shared__ float buf[2][NT / 64];
   extern __shared__ float teams_dw[];
   const int K = a.K, R = a.teams, threads = blockDim.x / R;
+  if ((int)blockIdx.x >= a.groups) {
+    direct_column_sums<Pieces<BF16>::P, NT>(
+        a.M, ((int)blockIdx.x - a.groups) * 64, a.dweight,
+        [&](int64_t m, int c, float (&v)[Pieces<BF16>::P]) {
+          float d[Pieces<BF16>::P], x[Pieces<BF16>::P];
+          load_piece<BF16>(a.dy, m * K + c, d);
+          load_piece<BF16>(a.h, m * K + c, x);
+          const float rstd = a.rstd[m];
+#pragma unroll
+          for (int i = 0; i < Pieces<BF16>::P; ++i) v[i] = __builtin_fmaf(d[i], x[i] * rstd, v[i]);
+        });
+    return;
+  }
   const int team = threadIdx.x / threads, t = threadIdx.x - team * threads;
   const int wave = t >> 6, waves = threads >> 6;
   int col[C];
@@ -366,7 +416,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_backward_kernel(NormBwdArgs a) {
     for (int c = 0; c < C; ++c)
       if (col[c] < K && a.dh) dh[c].load(a.dh, m * K + col[c]);
   };
-  const int64_t step = (int64_t)gridDim.x * R;
+  const int64_t step = (int64_t)a.groups * R;
   int64_t m = (int64_t)blockIdx.x * R + team;
   if (AHEAD && m < a.M) {
     fetch(m);
@@ -418,6 +468,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_backward_kernel(NormBwdArgs a) {
     }
     if (AHEAD && m + step < a.M) fetch_dh(m + step);
   }
+  if (!a.part) return;
   if (R > 1) {
     if (team > 0) {
 #pragma unroll
@@ -441,12 +492,14 @@ struct ActBwdArgs {
   const uint16_t* pre;  // unused with DG_ACT_NONE
   uint8_t* codes;
   ScaleOut so;
-  float* part;          // [row groups][N] partial dbias; NULL: no dbias
+  float* part;          // [row groups][N] partial dbias; NULL: none
+  float* dbias;         // part == NULL: written by workgroups from strips * groups on, if any
   int64_t M;
   int64_t rows;         // rows per row group
   int32_t N;
   int32_t act;
   int32_t strips;       // column strips of 1024
+  int32_t groups;       // row groups
 };
 
 // A workgroup of four waves takes a strip of 1024 columns (8 blocks of 128, 8 lanes each)
@@ -455,6 +508,20 @@ struct ActBwdArgs {
 __global__ void __launch_bounds__(256) act_backward_kernel(ActBwdArgs a) {
   __shared__ float sums[3][1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if ((int)blockIdx.x >= a.strips * a.groups) {
+    direct_column_sums<8, 256>(a.M, ((int)blockIdx.x - a.strips * a.groups) * 64, a.dbias,
+                               [&](int64_t m, int c, float (&v)[8]) {
+                                 float d[8], x[8];
+                                 load_piece<true>(a.dc, m * a.N + c, d);
+                                 if (a.act != DG_ACT_NONE) {
+                                   load_piece<true>(a.pre, m * a.N + c, x);
+                                   act_backward(d, x, a.act);
+                                 }
+#pragma unroll
+                                 for (int i = 0; i < 8; ++i) v[i] += d[i];
+                               });
+    return;
+  }
   const int strip = blockIdx.x % a.strips, group = blockIdx.x / a.strips;
   const int in_strip = (lane >> 3) * 128 + (lane & 7) * Pieces<true>::P;
   const int col = strip * 1024 + in_strip;

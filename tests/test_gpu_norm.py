@@ -202,7 +202,8 @@ def test_norm_rows_past_32_bit_offsets():
 # ---------------------------------------------------------------- backward of the norm
 
 @pytest.mark.parametrize("M,K", [(1, 128), (1, 7168), (3, 384), (7, 1152), (257, 2048), (64, 7168),
-                                 (3, 16512), (5, 18432), (2, 32768), (3000, 256)])
+                                 (3, 16512), (5, 18432), (2, 32768), (3000, 256), (300, 16512), (256, 1024),
+                                 (600, 9216)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_norm_backward(M, K, dtype):
     h, dy, dh = (hidden(100 * s + M + K, M, K, dtype) for s in range(3))
@@ -267,7 +268,7 @@ def test_backward_of_no_rows_writes_zeros():
 # ---------------------------------------------------------------- backward of the epilogue
 
 @pytest.mark.parametrize("M,N", [(1, 128), (1, 18432), (3, 384), (5, 1024), (130, 2048), (257, 1152),
-                                 (4100, 256), (64, 7168)])
+                                 (4100, 256), (64, 7168), (130, 12288)])
 @pytest.mark.parametrize("act", ops.ACTS)
 def test_act_backward(M, N, act):
     g = torch.Generator().manual_seed(M + N)
