@@ -1268,8 +1268,10 @@ dg_status gemm_epilogue(const void* A, const void* B, const void* sfA, int32_t s
 
 // ---------------------------------------------------------------- norm and its backward
 
-// A row's threads hold 16 values each, in one chunk up to K = 8192, else two.
-int norm_chunks(int64_t K) { return K > 8192 ? 2 : 1; }
+// A row's threads, at most 512, hold 16 values each in one to four chunks. (4096 x 18432,
+// three chunks against two of up to 1024 threads: backward bf16 144 and 160 us, fp32 186 and
+// 262; forward bf16 100 and 90, fp32 92 and 102.)
+int norm_chunks(int64_t K) { return (int)((K + 8191) / 8192); }
 int norm_threads(int64_t K) {
   const int64_t t = (K / 16 + norm_chunks(K) - 1) / norm_chunks(K);
   return (int)((t + 63) / 64 * 64);
@@ -1291,14 +1293,17 @@ int64_t even_grid(int64_t rows, int64_t most) {
 }
 
 // Calls f with the compile-time form of a norm kernel for these types and K:
-// f(bf16 x?, bf16 weights?, chunks, thread bound).
+// f(bf16 x?, bf16 weights?, chunks).
 template <class F>
 void norm_form(bool x_bf16, bool w_bf16, int64_t K, F f) {
   auto by_k = [&](auto xb, auto wb) {
     using std::integral_constant;
-    if (norm_chunks(K) == 1) f(xb, wb, integral_constant<int, 1>{}, integral_constant<int, 512>{});
-    else if (K <= 16384) f(xb, wb, integral_constant<int, 2>{}, integral_constant<int, 512>{});
-    else f(xb, wb, integral_constant<int, 2>{}, integral_constant<int, 1024>{});
+    switch (norm_chunks(K)) {
+      case 1: f(xb, wb, integral_constant<int, 1>{}); break;
+      case 2: f(xb, wb, integral_constant<int, 2>{}); break;
+      case 3: f(xb, wb, integral_constant<int, 3>{}); break;
+      default: f(xb, wb, integral_constant<int, 4>{}); break;
+    }
   };
   auto by_w = [&](auto xb) {
     if (w_bf16) by_k(xb, std::true_type{});
@@ -1389,11 +1394,14 @@ dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dt
   NormArgs a{x, residual, weight, h, rstd, (uint8_t*)codes,
              ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(K / 128)}, M, (int32_t)K, eps};
   const int nt = norm_threads(K);
-  // 16 waves per CU hold the rows in flight and the next ones
-  const dim3 grid((unsigned)even_grid(M, nt < 1024 ? kCUs * (1024 / nt) : kCUs)), block((unsigned)nt);
-  norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c, auto n) {
-    constexpr bool ahead = n.value <= 512 || xb.value;
-    hipLaunchKernelGGL((rmsnorm_kernel<xb.value, wb.value, c.value, n.value, ahead>), grid, block, 0,
+  // 16 waves per CU hold the rows in flight and the next ones; 8 with several chunks a thread
+  // (4096 x 9216 bf16, 5 waves a row: 48.8 us with one workgroup per CU, 54.5 with three;
+  // 4096 x 5120: 37.0 and 26.8)
+  const int resident = norm_chunks(K) == 1 ? 1024 / nt : 1;
+  const dim3 grid((unsigned)even_grid(M, kCUs * resident)), block((unsigned)nt);
+  norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
+    constexpr bool ahead = c.value <= (xb.value ? 3 : 2);  // what 256 registers hold
+    hipLaunchKernelGGL((rmsnorm_kernel<xb.value, wb.value, c.value, ahead>), grid, block, 0,
                        (hipStream_t)stream, a);
   });
   return launched("rmsnorm_kernel");
@@ -1429,10 +1437,10 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
   }
   NormBwdArgs a{dy, dh, h, weight, rstd, dx, part, dweight, M, (int32_t)K, (int32_t)R, (int32_t)G};
   const unsigned grid = (unsigned)(G + (direct ? K / 64 : 0));
-  norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c, auto n) {
-    constexpr bool ahead = n.value <= 512;
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<xb.value, wb.value, c.value, n.value, ahead>),
-                       dim3(grid), dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
+  norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
+    constexpr bool ahead = c.value <= 2;  // what 256 registers hold
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<xb.value, wb.value, c.value, ahead>), dim3(grid),
+                       dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
   });
   s = launched("rmsnorm_backward_kernel");
   return s == DG_OK && !direct ? launch_column_sum(part, dweight, G, K, st) : s;
@@ -1454,10 +1462,11 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
   const hipStream_t st = (hipStream_t)stream;
   if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, N, st) : DG_OK;
   const int64_t strips = (N + 1023) / 1024;
-  // row groups: about 16 workgroups per CU (bf16 4096 x 18432, gelu and its column sums:
-  // 78.3 us with 228 groups, 78.4 with 170, 81.1 with 113), at least 4 rows (one per wave)
-  int64_t groups = (16 * kCUs + strips - 1) / strips;
-  if (groups > (M + 3) / 4) groups = (M + 3) / 4;
+  // row groups: about 8 workgroups per CU, at least 8 rows (two per wave) each (gelu with its
+  // column sums, at least 4 / 8 / 16 rows: 4096 x 2048 19.9 / 16.9 / 16.2 us, 1000 x 512
+  // 6.7 / 7.8 / 10.1; 4096 x 18432, 16 / 8 workgroups per CU: 80.1 / 78.8)
+  int64_t groups = (8 * kCUs + strips - 1) / strips;
+  if (groups > (M + 7) / 8) groups = (M + 7) / 8;
   const int64_t rows = ((M + groups - 1) / groups + 3) / 4 * 4;
   groups = (M + rows - 1) / rows;
   const bool direct = dbias && M <= kDirectRows && M * N <= kDirectActValues, sum = dbias && !direct;

@@ -270,7 +270,8 @@ __device__ __forceinline__ float row_sum(float v, float* buf, int wave, int wave
   return s;
 }
 
-constexpr int kNormMaxK = 32768;  // two 16-value chunks in each of 1024 threads
+constexpr int kNormThreads = 512;                // most threads of a workgroup
+constexpr int kNormMaxK = 4 * 16 * kNormThreads;  // four 16-value chunks in each
 
 struct NormArgs {
   const void* x;
@@ -293,11 +294,11 @@ __device__ __forceinline__ int norm_col(int c, int threads, int t) {
 
 // Workgroup b takes rows b, b + G, b + 2G, ... (G workgroups), its threads C chunks of 16
 // values each. AHEAD: the weights stay in registers and the next row is loaded before the
-// barrier of this one; otherwise (1024 threads, which leave 128 registers each, fp32) both
-// are loaded where they are used.
-template <bool BF16, bool WBF, int C, int NT, bool AHEAD>
-__global__ void __launch_bounds__(NT) rmsnorm_kernel(NormArgs a) {
-  __shared__ float buf[2][NT / 64];
+// barrier of this one; otherwise (long rows, whose values fill the registers) both are loaded
+// where they are used.
+template <bool BF16, bool WBF, int C, bool AHEAD>
+__global__ void __launch_bounds__(kNormThreads) rmsnorm_kernel(NormArgs a) {
+  __shared__ float buf[2][kNormThreads / 64];
   const int K = a.K, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   int col[C];
   Weight16<BF16, WBF> w[C];
@@ -368,15 +369,15 @@ struct NormBwdArgs {
 // The weights and the column sums of dweight stay in registers; the teams' sums meet in LDS
 // at the end, in team order, so that a workgroup leaves one row of partials. AHEAD: the next
 // row's h and dy are loaded before the barrier of this one, and its dh behind it; otherwise
-// (1024 threads, which leave 128 registers each) a row's values are kept as loaded, and
-// the weights are read again where they are used.
-template <bool BF16, bool WBF, int C, int NT, bool AHEAD>
-__global__ void __launch_bounds__(NT) rmsnorm_backward_kernel(NormBwdArgs a) {
-  __shared__ float buf[2][NT / 64];
+// (long rows) a row's values are kept as loaded, and the weights are read again where they
+// are used.
+template <bool BF16, bool WBF, int C, bool AHEAD>
+__global__ void __launch_bounds__(kNormThreads) rmsnorm_backward_kernel(NormBwdArgs a) {
+  __shared__ float buf[2][kNormThreads / 64];
   extern __shared__ float teams_dw[];
   const int K = a.K, R = a.teams, threads = blockDim.x / R;
   if ((int)blockIdx.x >= a.groups) {
-    direct_column_sums<Pieces<BF16>::P, NT>(
+    direct_column_sums<Pieces<BF16>::P, kNormThreads>(
         a.M, ((int)blockIdx.x - a.groups) * 64, a.dweight,
         [&](int64_t m, int c, float (&v)[Pieces<BF16>::P]) {
           float d[Pieces<BF16>::P], x[Pieces<BF16>::P];
