@@ -1428,7 +1428,8 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
   int64_t R = nt < 512 ? 512 / nt : 1;
   if (R > (M + kCUs - 1) / kCUs) R = (M + kCUs - 1) / kCUs;
   const int64_t G = even_grid((M + R - 1) / R, kCUs);
-  const bool direct = M <= kDirectRows;
+  // a dx in the place of dy or h would be written while the column sums read them
+  const bool direct = M <= kDirectRows && dx != dy && dx != h;
   float* part = nullptr;
   if (!direct) {
     uint32_t* counters = nullptr;

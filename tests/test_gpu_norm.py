@@ -237,6 +237,22 @@ def test_norm_backward_in_place(which):
     assert torch.equal(got, want) and torch.equal(gotw, wantw)
 
 
+@pytest.mark.parametrize("M,K", [(1, 7168), (64, 512), (200, 7168), (256, 16512)])
+@pytest.mark.parametrize("which", ["dy", "dh", "h"])
+def test_norm_backward_in_place_of_few_rows(M, K, which):
+    # the sums of few rows read the inputs again: dx must not overwrite them before
+    h, dy, dh = (hidden(s, M, K, F32) for s in (25, 26, 27))
+    w, rstd = weights(28, K, F32), torch.rand(M)
+    want, _ = dg().rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda(), rstd.cuda(), dh=dh.cuda())
+    t = dict(dy=dy.cuda(), h=h.cuda(), dh=dh.cuda())
+    got, gotw = dg().rmsnorm_backward(t["dy"], t["h"], w.cuda(), rstd.cuda(), dh=t["dh"], dx=t[which])
+    torch.cuda.synchronize()
+    _, wantw, _, bw = ops.rmsnorm_backward(dy.double().numpy(), h.double().numpy(), w.double().numpy(),
+                                           rstd.double().numpy(), dh.double().numpy())
+    assert torch.equal(got, want)
+    assert np.all(np.abs(gotw.double().cpu().numpy() - wantw) <= bw + 1e-45)
+
+
 def test_norm_backward_is_the_difference_quotient_of_the_forward_norm():
     # directional difference of sum(dy * y) on the fp64 formula with the forward's own rstd
     M, K = 40, 1024
