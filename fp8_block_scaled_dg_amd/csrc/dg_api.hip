@@ -14,6 +14,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <set>
@@ -1225,6 +1226,19 @@ dg_status dg_describe_config(int32_t kind, int64_t M, int64_t N, int64_t K, int3
 namespace dg {
 namespace {
 
+// f(), a C++ exception of the host code (std::bad_alloc of the workspace tables) turned into
+// a status: none leaves a C entry.
+template <class F>
+dg_status no_throw(F f) noexcept {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(DG_ERR_LAUNCH, "host code: %s", e.what());
+  } catch (...) {
+    return fail(DG_ERR_LAUNCH, "host code: an unknown exception");
+  }
+}
+
 // ---------------------------------------------------------------- GEMM with a fused epilogue
 
 bool known_dtype(int32_t t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
@@ -1337,6 +1351,14 @@ dg_status launched(const char* what) {
 }
 
 // out[n] = sum over R rows of part[R][N] (N % 32 == 0); R = 0 writes zeros
+// The stream's workspace as `count` partial sums.
+dg_status get_partials(hipStream_t st, int64_t count, float** part) {
+  return no_throw([&] {
+    uint32_t* counters = nullptr;
+    return get_workspace(st, (size_t)count * sizeof(float), 0, part, &counters);
+  });
+}
+
 dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N, hipStream_t st) {
   hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)(N / 32)), dim3(256), 0, st, part, out, (int)R,
                      (int)N);
@@ -1359,7 +1381,9 @@ dg_status dg_fp8_gemm_nt_bias_act(const void* A, const void* B, void* C, const v
   ep.act = activation;
   ep.residual = (const uint16_t*)residual;
   ep.pre = (uint16_t*)pre;
-  return gemm_epilogue(A, B, sfA, sfA_packed, sfB, M, N, K, C, false, bias_dtype, ep, stream);
+  return no_throw([&] {
+    return gemm_epilogue(A, B, sfA, sfA_packed, sfB, M, N, K, C, false, bias_dtype, ep, stream);
+  });
 }
 
 dg_status dg_fp8_gemm_nt_bias_act_fp8(const void* A, const void* B, void* codes, void* sf,
@@ -1375,7 +1399,9 @@ dg_status dg_fp8_gemm_nt_bias_act_fp8(const void* A, const void* B, void* codes,
   ep.pre = (uint16_t*)pre;
   ep.codes = (uint8_t*)codes;
   ep.so = ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)};
-  return gemm_epilogue(A, B, sfA, sfA_packed, sfB, M, N, K, nullptr, true, bias_dtype, ep, stream);
+  return no_throw([&] {
+    return gemm_epilogue(A, B, sfA, sfA_packed, sfB, M, N, K, nullptr, true, bias_dtype, ep, stream);
+  });
 }
 
 dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dtype,
@@ -1432,8 +1458,7 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
   const bool direct = M <= kDirectRows && dx != dy && dx != h;
   float* part = nullptr;
   if (!direct) {
-    uint32_t* counters = nullptr;
-    s = get_workspace(st, (size_t)(G * K) * sizeof(float), 0, &part, &counters);
+    s = get_partials(st, G * K, &part);
     if (s != DG_OK) return s;
   }
   NormBwdArgs a{dy, dh, h, weight, rstd, dx, part, dweight, M, (int32_t)K, (int32_t)R, (int32_t)G};
@@ -1473,8 +1498,7 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
   const bool direct = dbias && M <= kDirectRows && M * N <= kDirectActValues, sum = dbias && !direct;
   float* part = nullptr;
   if (sum) {
-    uint32_t* counters = nullptr;
-    s = get_workspace(st, (size_t)(groups * N) * sizeof(float), 0, &part, &counters);
+    s = get_partials(st, groups * N, &part);
     if (s != DG_OK) return s;
   }
   ActBwdArgs a{(const uint16_t*)dc, (const uint16_t*)pre, (uint8_t*)codes,
