@@ -76,48 +76,66 @@ __device__ __forceinline__ void epi_store8(v4u res, uint16_t* C, int64_t off, fl
 template <int BN>
 constexpr int kEpiPitch = BN + 4;
 
-// Finishes rows row0 .. row0 + ROWS - 1 of the fp32 tile of columns n0 .. n0 + BN - 1, held
-// in out[ROWS][kEpiPitch<BN>] (all threads of the workgroup, after a barrier): 8 columns of
-// a row per thread and step. kEpiFp8: BN = 128, 16 neighbouring lanes hold a row's 1x128
-// block.
+// Finishes ROWS rows of the fp32 tile of columns n0 .. n0 + BN - 1, held in
+// out[ROWS][kEpiPitch<BN>]: 8 columns of a row per thread and step. load() fetches bias and
+// residual, which needs nothing of the product and may be called long before finish().
+// kEpiFp8: BN = 128, 16 neighbouring lanes hold a row's 1x128 block.
 template <int BN, int NT, int EPI, int ROWS>
-__device__ __forceinline__ void epi_finish_tile(const Problem& p, int64_t n0, const float* out,
-                                                const Epilogue& ep, int row0) {
+struct EpiTile {
   static_assert(EPI != kEpiFp8 || BN == 128, "a scale block per tile row");
-  constexpr int LPR = BN / 8;  // lanes per row
-  static_assert(64 % LPR == 0 && (ROWS * LPR) % 64 == 0, "whole rows per wave");
-  const int64_t N = p.N;
-#pragma unroll 1
-  for (int c = threadIdx.x; c < ROWS * LPR; c += NT) {
-    const int rl = c / LPR, row = row0 + rl, col0 = (c % LPR) * 8;
-    const int64_t col = n0 + col0, off = row * N + col;
-    if (row >= p.M || col >= N) continue;
-    v4u res = {0, 0, 0, 0};
-    if (EPI == kEpiBf16 && ep.residual)
-      res = __builtin_nontemporal_load((const v4u*)(ep.residual + off));
-    float b[8], x[8];
-    epi_bias8(ep, col, b);
-    const v4f lo = *(const v4f*)(out + rl * kEpiPitch<BN> + col0);
-    const v4f hi = *(const v4f*)(out + rl * kEpiPitch<BN> + col0 + 4);
+  static constexpr int LPR = BN / 8;  // lanes per row
+  static constexpr int STEPS = (ROWS * LPR + NT - 1) / NT;
+  static_assert(64 % LPR == 0 && (ROWS * LPR) % 64 == 0 && NT % LPR == 0, "whole rows per wave");
+  v4u res[EPI == kEpiBf16 ? STEPS : 1];
+  float b[8];
+
+  __device__ __forceinline__ void load(const Problem& p, int64_t n0, const Epilogue& ep, int row0) {
+    const int64_t col = n0 + (int)(threadIdx.x % LPR) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
-    epi_act8(ep, b, off, x);
-    if (EPI == kEpiBf16) {
-      epi_store8(res, p.C, off, x);
-    } else {
-      float m = 0.f;
+    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+    if (col < p.N) epi_bias8(ep, col, b);
+    if (EPI != kEpiBf16) return;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 16));
-      const int e = scale_exp(ep.so, m);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], -e);
-      *(uint2*)(ep.codes + off) =
-          make_uint2(quant_e4m3fn_x4(x[0], x[1], x[2], x[3]), quant_e4m3fn_x4(x[4], x[5], x[6], x[7]));
-      if (col0 == 0) store_scale(ep.so, row, (int)(col >> 7), e);
+    for (int i = 0; i < STEPS; ++i) {
+      const int rl = (threadIdx.x + i * NT) / LPR;
+      res[i] = v4u{0, 0, 0, 0};
+      if (ep.residual && rl < ROWS && row0 + rl < p.M && col < p.N)
+        res[i] = __builtin_nontemporal_load((const v4u*)(ep.residual + (row0 + rl) * p.N + col));
     }
   }
-}
+
+  // all threads of the workgroup, after a barrier behind the writes of out
+  __device__ __forceinline__ void finish(const Problem& p, int64_t n0, const float* out,
+                                         const Epilogue& ep, int row0) {
+    const int col0 = (int)(threadIdx.x % LPR) * 8;
+    const int64_t col = n0 + col0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int rl = (threadIdx.x + i * NT) / LPR, row = row0 + rl;
+      if (rl >= ROWS || row >= p.M || col >= p.N) continue;
+      const int64_t off = row * p.N + col;
+      float x[8];
+      const v4f lo = *(const v4f*)(out + rl * kEpiPitch<BN> + col0);
+      const v4f hi = *(const v4f*)(out + rl * kEpiPitch<BN> + col0 + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = lo[j], x[4 + j] = hi[j];
+      epi_act8(ep, b, off, x);
+      if (EPI == kEpiBf16) {
+        epi_store8(res[i], p.C, off, x);
+      } else {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+        m = max8(m);
+        const int e = scale_exp(ep.so, fmaxf(m, dppf<kDppMirror16>(m)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = ldexpf(x[j], -e);
+        *(uint2*)(ep.codes + off) =
+            make_uint2(quant_e4m3fn_x4(x[0], x[1], x[2], x[3]), quant_e4m3fn_x4(x[4], x[5], x[6], x[7]));
+        if (col0 == 0) store_scale(ep.so, row, (int)(col >> 7), e);
+      }
+    }
+  }
+};
 
 }  // namespace dg

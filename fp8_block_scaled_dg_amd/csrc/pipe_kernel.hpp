@@ -855,14 +855,13 @@ __device__ __forceinline__ void pipe_store_epi(const Problem& p, const TileView&
           keep[2 * h + k][i] = x[k][i];
           m = fmaxf(m, fabsf(x[k][i]));
         }
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 8));
+        m = max8(m);
         if (ch == 0) pipe_rmax[wave][16 * h + 8 * k + rr] = m;
       }
     }
   }
   if (EPI == kEpiFp8) {
-    __syncthreads();
+    lds_barrier();  // the stores of pre stay in flight
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t row = row0 + 8 * k;

@@ -57,7 +57,7 @@ struct RingCfg {
   static constexpr int SROWS = BM <= 64 ? 4 : 8;  // 16-row groups whose scales are staged
   static constexpr int STAGE = OFF_S + SROWS * 256;
   static constexpr int SMAX = TM * TN <= 4 ? 8 : 2;  // splits whose partials fit the registers
-  static constexpr int ROWS = BM < 32 ? BM : 32;  // rows per pass of the epilogue
+  static constexpr int ROWS = BM < 64 ? BM : 64;  // rows per pass of the epilogue
   static_assert(SROWS <= W && BM <= 16 * SROWS, "scale rows");
   static_assert(BM <= 128 && B_DMA >= 1 && W % 4 == 0, "DMA split");
   static_assert(ROWS * kEpiPitch<BN> * 4 <= OFF_S, "a pass of the fp32 tile fits a stage");
@@ -237,6 +237,10 @@ __global__ void __launch_bounds__(Cfg::NT) ring_kernel(RingArgs args) {
   }
   src.sfb = (ring_const)(uintptr_t)(p.sfB + (n0 / kKBlock) * KB + kb0);
 
+  constexpr int ROWS = Cfg::ROWS;
+  EpiTile<BN, Cfg::NT, EPI, ROWS> epi;
+  epi.load(p, n0, args.ep, (int)m0);
+
   v4f acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -298,13 +302,13 @@ __global__ void __launch_bounds__(Cfg::NT) ring_kernel(RingArgs args) {
 
   // the fp32 tile through LDS, ROWS rows at a time. Every DMA has landed: the last step
   // waited for all of them.
-  constexpr int ROWS = Cfg::ROWS;
   const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
   float* out = (float*)ring_stage<Cfg::STAGE, 0>;
 #pragma unroll
   for (int h = 0; h < Cfg::BM / ROWS; ++h) {
     if (ROWS * h >= M) break;
-    __syncthreads();
+    lds_barrier();
+    if (h > 0) epi.load(p, n0, args.ep, (int)m0 + ROWS * h);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int row = (wm * TM + i) * 16 - ROWS * h;  // of the pass
@@ -313,8 +317,8 @@ __global__ void __launch_bounds__(Cfg::NT) ring_kernel(RingArgs args) {
       for (int j = 0; j < TN; ++j)
         *(v4f*)(out + (row + l16) * kEpiPitch<BN> + (wn * TN + j) * 16 + 4 * g) = acc[i][j];
     }
-    __syncthreads();
-    epi_finish_tile<BN, Cfg::NT, EPI, ROWS>(p, n0, out, args.ep, (int)m0 + ROWS * h);
+    lds_barrier();
+    epi.finish(p, n0, out, args.ep, (int)m0 + ROWS * h);
   }
 }
 
