@@ -491,11 +491,14 @@ dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
 // epilogue; the pairs; for S > 1 the partials' trip through memory and the last split's sum
 // over them; for more tiles than CUs, further rounds at the rate that L2 leaves to each.
 // bf16 output with residual, gelu:         us, S = 1      2      4      8
-//   M =  64,  4096 columns, K =  7168, 64 x 128 tiles  27.2   19.5   15.6   16.2
-//   M =  64,  8192 columns, K =  2048, 64 x 128        12.2   12.6   14.7
-//   M =   1,  2048 columns, K =  4096, 16 x 128        10.7    8.9    8.0    7.8
-//   M = 256,  4096 columns, K =  7168, 64 x  64        20.5
-//   M = 1008, 4096 columns, K =  7168, 128 x 128       45.1 (64 x 128: 56.5)
+//   M =  64,  2112 columns, K =  7168, 64 x  64 tiles  19.8   14.0   11.0   10.6
+//   M =  64,  2112 columns, K =  7168, 64 x 128        26.3   18.5   14.3   13.8
+//   M =  64,  8192 columns, K =  2048, 64 x  64         9.2    9.3
+//   M =  32,  1024 columns, K =  8192, 32 x  64        15.8   11.2    8.8    8.2
+//   M =   1,  2048 columns, K =  4096, 16 x  64         8.1    7.4    6.6    6.8
+//   M = 256,  4096 columns, K =  7168, 64 x  64        21.1 (64 x 128: 27.1, 20.3 with S = 2)
+//   M = 512,  4096 columns, K =  7168, 64 x 128        28.6 (128 x 128: 40.8, 30.2 with S = 2)
+//   M = 1008, 4096 columns, K =  7168, 128 x 128       43.2 (64 x 128: 54.4)
 struct RingPlan {
   int64_t S, KS;
   double time;
@@ -505,8 +508,8 @@ RingPlan ring_plan(int64_t tiles, int64_t KB, int BM, int BN, int most) {
   const bool n64 = BN == 64;
   const double start = BM == 128 ? 75 : 45;
   const double pair = BM == 128 ? 13 : BM == 64 ? (n64 ? 5.5 : 8.4) : BM == 32 ? (n64 ? 3.6 : 6) : (n64 ? 2.4 : 4);
-  const double fixed = BM >= 64 ? 25 : BM == 32 ? 18 : 12;
-  const double each = BM == 128 ? 15 : BM == 64 ? 7.5 : BM == 32 ? 4 : 2.2;
+  const double fixed = BM >= 64 ? 10 : BM == 32 ? 6 : 8;
+  const double each = BM == 128 ? 12 : BM == 64 ? (n64 ? 4.2 : 7.5) : BM == 32 ? (n64 ? 2 : 3.5) : 1.4;
   const int64_t pairs = (KB + 1) / 2, rounds = (tiles + kCUs - 1) / kCUs;
   RingPlan best{1, KB, start + pair * (double)pairs};
   if (rounds > 1) best.time = start + (double)rounds * 1.2 * pair * (double)pairs + 30 * (double)(rounds - 1);
@@ -519,8 +522,8 @@ RingPlan ring_plan(int64_t tiles, int64_t KB, int BM, int BN, int most) {
 }
 
 // Tile kernel: 1 us per K-block and round of tiles, the epilogue of each round, and the tail
-// tiles' split (its partial tiles are 128 KB each). M = 512, 4096 columns, K = 7168: 42 us;
-// M = 4096, 7168 columns, K = 2048: 98 us.
+// tiles' split (its partial tiles are 128 KB each). M = 512, 4096 columns, K = 7168: 41 us;
+// M = 4096, 7168 columns, K = 2048: 92 us.
 double pipe_time(int64_t M, int64_t N, int64_t KB, int BM, int BN) {
   const int64_t tiles = (M + BM - 1) / BM * ((N + BN - 1) / BN);
   const TailSplit ts = pipe_tail_split(tiles, KB);

@@ -71,7 +71,7 @@ __device__ __forceinline__ void epi_store8(v4u res, uint16_t* C, int64_t off, fl
   __builtin_nontemporal_store(epi_pack8(v), (v4u*)(C + off));
 }
 
-// Row pitch, in floats, of the fp32 tile that the M <= 64 kernel leaves in LDS: 4 floats
+// Row pitch, in floats, of the fp32 tile that the ring kernel leaves in LDS: 4 floats
 // past BN spread the rows over the banks.
 template <int BN>
 constexpr int kEpiPitch = BN + 4;
