@@ -1491,11 +1491,12 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
   const hipStream_t st = (hipStream_t)stream;
   if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, N, st) : DG_OK;
   const int64_t strips = (N + 1023) / 1024;
-  // row groups: about 8 workgroups per CU, at least 8 rows (two per wave) each (gelu with its
-  // column sums, at least 4 / 8 / 16 rows: 4096 x 2048 19.9 / 16.9 / 16.2 us, 1000 x 512
-  // 6.7 / 7.8 / 10.1; 4096 x 18432, 16 / 8 workgroups per CU: 80.1 / 78.8)
+  // row groups: about 8 workgroups per CU (gelu with its column sums, 4096 x 18432: 78.8 us,
+  // with 16 80.1), of at least 8 rows, two per wave, or 4 where 8 would leave CUs idle
+  // (at least 4 / 8 / 16: 4096 x 2048 19.9 / 16.9 / 16.2 us, 1000 x 512 6.7 / 7.8 / 10.1)
+  const int64_t least = (M + 7) / 8 * strips < kCUs ? 4 : 8;
   int64_t groups = (8 * kCUs + strips - 1) / strips;
-  if (groups > (M + 7) / 8) groups = (M + 7) / 8;
+  if (groups > (M + least - 1) / least) groups = (M + least - 1) / least;
   const int64_t rows = ((M + groups - 1) / groups + 3) / 4 * 4;
   groups = (M + rows - 1) / rows;
   const bool direct = dbias && M <= kDirectRows && M * N <= kDirectActValues, sum = dbias && !direct;
