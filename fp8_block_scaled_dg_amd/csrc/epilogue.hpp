@@ -87,13 +87,17 @@ struct EpiTile {
   static constexpr int STEPS = (ROWS * LPR + NT - 1) / NT;
   static_assert(64 % LPR == 0 && (ROWS * LPR) % 64 == 0 && NT % LPR == 0, "whole rows per wave");
   v4u res[EPI == kEpiBf16 ? STEPS : 1];
-  float b[8];
+  v4u bias[2];  // as stored: unpacking it here would wait for it
 
   __device__ __forceinline__ void load(const Problem& p, int64_t n0, const Epilogue& ep, int row0) {
     const int64_t col = n0 + (int)(threadIdx.x % LPR) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 0.f;
-    if (col < p.N) epi_bias8(ep, col, b);
+    bias[0] = bias[1] = v4u{0, 0, 0, 0};
+    if (ep.bias && col < p.N) {
+      const v4u* src = ep.bias_bf16 ? (const v4u*)((const uint16_t*)ep.bias + col)
+                                    : (const v4u*)((const float*)ep.bias + col);
+      bias[0] = src[0];
+      if (!ep.bias_bf16) bias[1] = src[1];
+    }
     if (EPI != kEpiBf16) return;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
@@ -109,6 +113,12 @@ struct EpiTile {
                                          const Epilogue& ep, int row0) {
     const int col0 = (int)(threadIdx.x % LPR) * 8;
     const int64_t col = n0 + col0;
+    float b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = bias[0][j / 2], half = j & 1 ? u & 0xFFFF0000u : u << 16;
+      b[j] = __uint_as_float(ep.bias_bf16 ? half : bias[j / 4][j % 4]);
+    }
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       const int rl = (threadIdx.x + i * NT) / LPR, row = row0 + rl;

@@ -11,6 +11,10 @@
 // CU reaches grew with it: 32 workgroups on [4096][7168], 24.7 against 14.0 us.) D stages of
 // a pair of blocks keep 2 (D - 1) blocks in flight whatever the registers hold: 96 KB per CU
 // at D = 3, BN = 128.
+// What bounds it: one CU takes in about 42 KB/us (64 x 18432 x 7168, FP8 output: 144 tiles on as
+// many CUs, 28 KB/us of B and 14 of A each, 39.8 us), HBM gives 20 KB/us of B to each of 256
+// (64 x 32768 x 7168: 43.9 us). Splitting K pays while it brings idle CUs in (64 x 16384 x 7168
+// in two halves: 28.5 us).
 // Per pair: wait for this wave's DMAs of it (vmcnt), one barrier (every wave's DMAs of the
 // pair have landed and every wave is done with the previous pair), refill the previous
 // pair's stage, then per block and 16x16 tile one v_mfma_f32_16x16x128_f8f6f4 and the

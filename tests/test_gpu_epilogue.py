@@ -90,6 +90,27 @@ def test_bias_and_residual_bitwise(M, N, K):
         assert np.array_equal(out.result(), oracle.bf16_rne(c)), "c"
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 16512, 6272), (16, 20464, 5120), (17, 18432, 5760), (33, 24576, 4224),
+                                   (64, 16640, 6400), (64, 32640, 3200)])
+def test_large_b_bitwise(M, N, K):
+    # 129 to 255 column tiles of a B of about 100 MB, with up to 64 rows
+    A, B, sfA, sfB, r = operands(M, N, K, M + N + K)
+    bias, residual = small_values(1, N, BF), small_values(2, (M, N), BF)
+    out, pre = gu.Guarded((M, N), 5), gu.Guarded((M, N), 6)
+    args = (gu.codes(A), gu.codes(B), out.out, gu.dev(sfA), gu.dev(sfB))
+    gu.announce(f"large B M={M} N={N} K={K}")
+    for _ in range(2):
+        out.out.zero_(), pre.out.zero_()
+        dg().fp8_gemm_nt_bias_act(*args, bias=bias.cuda(), residual=residual.cuda(), pre=pre.out)
+        torch.cuda.synchronize()
+        assert out.guards_intact() and pre.guards_intact(), "write outside an output"
+        z = r + bias.double().numpy()
+        c = z + residual.double().numpy()
+        assert np.array_equal(c.astype(np.float32), c), "the case is meant to be exact in fp32"
+        assert np.array_equal(pre.result(), oracle.bf16_rne(z)), "pre"
+        assert np.array_equal(out.result(), oracle.bf16_rne(c)), "c"
+
+
 @pytest.mark.parametrize("M,N,K", [(17, 2112, 7168), (64, 256, 896), (130, 4096, 512), (1000, 1040, 1024)])
 @pytest.mark.parametrize("act", ops.ACTS[1:])
 def test_activation(M, N, K, act):
