@@ -1429,7 +1429,8 @@ dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dt
   const int resident = norm_chunks(K) == 1 ? 1024 / nt : 1;
   const dim3 grid((unsigned)even_grid(M, kCUs * resident)), block((unsigned)nt);
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    constexpr bool ahead = c.value <= (xb.value ? 3 : 2);  // what 256 registers hold
+    // the next row ahead, where 256 registers hold it (4096 x 18432 bf16: 99.4 us, not ahead 114.1)
+    constexpr bool ahead = c.value <= (xb.value ? 3 : 2);
     hipLaunchKernelGGL((rmsnorm_kernel<xb.value, wb.value, c.value, ahead>), grid, block, 0,
                        (hipStream_t)stream, a);
   });
