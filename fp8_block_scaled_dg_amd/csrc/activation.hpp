@@ -99,8 +99,10 @@ __device__ __forceinline__ void act_backward(float (&d)[N], const float (&x)[N],
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float s = act_sigmoid(act_gelu_tanh_u(x[i]));
-      const float du = 1.5957691216057308f * __builtin_fmaf(0.134145f * x[i], x[i], 1.f);
-      d[i] *= __builtin_fmaf(x[i] * s * (1.f - s), du, s);
+      // t = x s (1 - s) before x^2: where x^2 overflows t is 0, and 0 times infinity is NaN
+      const float t = x[i] * s * (1.f - s);
+      const float du = __builtin_fmaf(0.134145f * x[i], t * x[i], t);
+      d[i] *= __builtin_fmaf(1.5957691216057308f, du, s);
     }
   }
 }
