@@ -562,11 +562,15 @@ enum RingForm { kRing64, kRing128, kRing128x128, kRingStream };
 
 int ring_bm(RingForm f, int64_t M) { return f == kRing128x128 ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 int ring_bn(RingForm f) { return f == kRing64 ? 64 : 128; }
+// splits whose partials fit the form's registers: SMAX of its RingCfg
+int ring_most(RingForm f, int64_t M) { return f == kRing128x128 || (f == kRingStream && M > 32) ? 2 : 8; }
 
-double ring_time(RingForm f, int64_t M, int64_t N, int64_t KB) {
+RingPlan ring_form_plan(RingForm f, int64_t M, int64_t N, int64_t KB) {
   const int BM = ring_bm(f, M), BN = ring_bn(f);
-  return ring_plan((M + BM - 1) / BM * ((N + BN - 1) / BN), KB, BM, BN, f == kRing128x128 ? 2 : 8).time;
+  return ring_plan((M + BM - 1) / BM * ((N + BN - 1) / BN), KB, BM, BN, ring_most(f, M));
 }
+
+double ring_time(RingForm f, int64_t M, int64_t N, int64_t KB) { return ring_form_plan(f, M, N, KB).time; }
 
 template <RingForm F, int EPI, bool PACKED>
 dg_status launch_ring_rows(const Problem& p, const Epilogue& ep, hipStream_t st) {
@@ -720,15 +724,24 @@ int select_config(int kind, int64_t m, int64_t M, int64_t n, int64_t k, int32_t 
   return find_cfg("pipe128x256");
 }
 
-// From this many bytes on, with up to 64 rows, B is streamed past the caches: the 256 MB MALL
-// cannot be expected to hold it from one use to the next. M = 64, FP8 output, 18432 x 7168
-// (132 MB): 35.8 us streamed, 40.2 not; 4096 x 7168 (29 MB), read over and over: 17.9 us
-// streamed, 15.6 not.
+// From this many bytes on, with up to 64 rows, B is streamed past the caches (the 256 MB MALL
+// cannot be expected to hold it from one use to the next), unless the product wants more K
+// splits than the streamed form can add: at 33 to 64 rows its 4 waves hold the partials of two.
+// us, streamed and through the caches, with so many weights in turn that none stays in one:
+//   M = 64, FP8 output, 18432 x  7168, one split     37.9, 42.4
+//                       12288 x  8192, two           28.1, 32.8
+//                       10240 x 10496, three         32.8, 29.4
+//                        7168 x 18432, four          48.4, 35.2
+//                        4096 x 28672, eight         70.6, 32.5
+//   M = 16, bf16 output, 7168 x 18432, four          24.6, 26.9
+// Below the bound: 11776 x 8192 (92 MB) 28.1, 32.9; 4096 x 7168 (28 MB), the same weights over
+// and over, 17.9, 15.6.
 constexpr int64_t kStreamB = int64_t(96) << 20;
 
-// The configuration of the dense GEMM with a fused epilogue, the one with the least estimated
-// time; -1 when K is beyond the kernels that have one. FP8 output needs 128-column tiles, so
-// that one workgroup holds whole 1x128 blocks of a row.
+// The configuration of the dense GEMM with a fused epilogue: for few rows and a large B by the
+// rule above, otherwise the one with the least estimated time; -1 when K is beyond the kernels
+// that have one. FP8 output needs 128-column tiles, so that one workgroup holds whole 1x128
+// blocks of a row.
 int select_epi_config(bool fp8, int64_t M, int64_t N, int64_t K) {
   const auto has = [&](int id) {
     const CfgEntry& c = kTable[id];
@@ -741,8 +754,11 @@ int select_epi_config(bool fp8, int64_t M, int64_t N, int64_t K) {
     if (id >= 0 && has(id)) return id;
   }
   const int64_t KB = K / kKBlock;
-  const char* name = "ring_n128_wide";
-  if (M > 64 || N * K < kStreamB) {
+  const char* name;
+  if (M <= 64 && N * K >= kStreamB) {
+    const bool fits = ring_form_plan(kRing128, M, N, KB).S <= ring_most(kRingStream, M);
+    name = fits ? "ring_n128_wide" : "ring_n128";
+  } else {
     struct { const char* name; double time; } c[] = {
         {"ring_n128", ring_time(kRing128, M, N, KB)},
         {"ring_n64", fp8 ? 1e30 : ring_time(kRing64, M, N, KB)},
