@@ -1369,7 +1369,6 @@ dg_status launched(const char* what) {
   return err == hipSuccess ? DG_OK : fail(DG_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(err));
 }
 
-// out[n] = sum over R rows of part[R][N] (N % 32 == 0); R = 0 writes zeros
 // The stream's workspace as `count` partial sums.
 dg_status get_partials(hipStream_t st, int64_t count, float** part) {
   return no_throw([&] {
@@ -1378,10 +1377,18 @@ dg_status get_partials(hipStream_t st, int64_t count, float** part) {
   });
 }
 
+// out[n] = sum over R rows of part[R][N] (N % 32 == 0); R = 0 writes zeros. A launch holds fewer
+// than 2^32 threads, 8 for each column: wider rows take several.
 dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N, hipStream_t st) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)(N / 32)), dim3(256), 0, st, part, out, (int)R,
-                     (int)N);
-  return launched("column_sum_kernel");
+  constexpr int64_t kMost = (int64_t)1 << 28;
+  for (int64_t n = 0; n < N; n += kMost) {
+    const int64_t cols = N - n < kMost ? N - n : kMost;
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, st,
+                       R > 0 ? part + n : part, out + n, (int)R, (int)N);
+    const dg_status s = launched("column_sum_kernel");
+    if (s != DG_OK) return s;
+  }
+  return DG_OK;
 }
 
 }  // namespace

@@ -354,7 +354,8 @@ dg_status dg_fp8_gemm_nt_bias_act_fp8(const void* A, const void* B, void* codes,
  *     call, which gives dA [M][K]
  *   dbias  fp32 [N] = sum_m p (before quantization; NULL: not computed)
  *   dc, pre  bf16 [M][N] (pre may be NULL with DG_ACT_NONE). relu'(0) = 0.
- * N % 128 == 0; M * N <= 2^40; dc, pre, codes and dbias 16-byte aligned, sf 4-byte aligned.
+ * N % 128 == 0; N <= 2^30, M * N <= 2^40; dc, pre, codes and dbias 16-byte aligned, sf 4-byte
+ * aligned.
  * Column sums are added in a fixed order. M == 0 writes zeros to dbias. Codes and scales of
  * a block holding an infinity or NaN are unspecified.
  */
