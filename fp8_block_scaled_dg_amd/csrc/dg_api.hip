@@ -532,6 +532,8 @@ double pipe_time(int64_t M, int64_t N, int64_t KB, int BM, int BN) {
   return 20 + (double)((tiles + kCUs - 1) / kCUs) * round;
 }
 
+constexpr int64_t kLaunchThreads = (int64_t)1 << 32;  // a launch holds fewer
+
 template <class Cfg, int EPI>
 dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t stream) {
   RingArgs a{};
@@ -543,7 +545,8 @@ dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t strea
   a.S = (int32_t)pl.S;
   a.KS = (int32_t)pl.KS;
   const int64_t grid = tiles * pl.S;
-  if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld", (long long)grid);
+  if (grid >= kLaunchThreads / Cfg::NT)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld workgroups", (long long)grid);
   if (pl.S > 1) {
     const size_t part = (size_t)grid * Cfg::BM * Cfg::BN * sizeof(float);
     const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
@@ -570,7 +573,12 @@ RingPlan ring_form_plan(RingForm f, int64_t M, int64_t N, int64_t KB) {
   return ring_plan((M + BM - 1) / BM * ((N + BN - 1) / BN), KB, BM, BN, ring_most(f, M));
 }
 
-double ring_time(RingForm f, int64_t M, int64_t N, int64_t KB) { return ring_form_plan(f, M, N, KB).time; }
+// Out of the question where a launch cannot hold a workgroup, of 512 threads at most, per tile.
+double ring_time(RingForm f, int64_t M, int64_t N, int64_t KB) {
+  const int BM = ring_bm(f, M), BN = ring_bn(f);
+  if ((M + BM - 1) / BM * ((N + BN - 1) / BN) >= kLaunchThreads / 512) return 1e30;
+  return ring_form_plan(f, M, N, KB).time;
+}
 
 template <RingForm F, int EPI, bool PACKED>
 dg_status launch_ring_rows(const Problem& p, const Epilogue& ep, hipStream_t st) {

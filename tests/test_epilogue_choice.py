@@ -59,3 +59,11 @@ def test_no_step_at_the_size_of_a_large_b(M):
     # either side of 96 MB, FP8 output: the same kernel for the same number of column tiles
     got = choices([(M, 4096, 24448), (M, 4096, 24576), (M, 5376, 18432), (M, 5504, 18432)])
     assert {v for k, v in got.items() if k[3]} == {"ring_n128"}
+
+
+def test_more_tiles_than_a_launch_holds_threads_for():
+    # the ring kernel launches a workgroup of 512 threads per tile, fewer than 2^32 in all
+    got = choices([(1 << 30, 16, 128), ((1 << 29) + 640, 256, 128), (1 << 20, 16, 128)])
+    assert got[(1 << 30, 16, 128, False)] == "pipe128x256"
+    assert got[((1 << 29) + 640, 256, 128, False)] == got[((1 << 29) + 640, 256, 128, True)] == "pipe128x256"
+    assert got[(1 << 20, 16, 128, False)].startswith("ring")
