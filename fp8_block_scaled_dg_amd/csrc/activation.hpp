@@ -8,10 +8,11 @@
 //                                                 x' = s + x s (1 - s) 2 u'
 // Phi is formed as Phi(-z) = t P(t) e^(-z^2/2) for z = |x|, t = 1 / (1 + 0.2687 z): 2 t P(t)
 // approximates e^(y^2) erfc(y), y = z / sqrt 2, with a polynomial of degree 8 fitted by
-// reweighted least squares to 2.1e-8 relative over y in [0, 12]. Both tails of gelu then
-// keep a relative accuracy of 5e-7 for |x| < 3 and 4e-6 for |x| < 13 (the rounding of x^2
-// in the exponent); 1 + erf(x / sqrt 2) would cancel to a few bits at x = -5, which a block
-// scaled by its own largest value would show. A NaN passes through all of them.
+// reweighted least squares; its fp32 coefficients are within 4.9e-8 relative over y in [0, 12].
+// Both tails of gelu then keep a relative accuracy of 7e-7 for |x| < 3 and 8.2e-6 for |x| < 13
+// (the rounding of x^2 in the exponent), with exp2 and reciprocal rounded to nearest; the
+// hardware's 1 ulp adds 1e-7 each. 1 + erf(x / sqrt 2) would cancel to a few bits at x = -5,
+// which a block scaled by its own largest value would show. A NaN passes through all of them.
 //
 // The backward kernel is as much bound by this arithmetic as by memory, so powers are single
 // v_exp_f32 on an argument scaled by log2 e (the library expf spends 12 more instructions on
