@@ -1320,9 +1320,16 @@ int norm_threads(int64_t K) {
 
 // Up to this many rows the backward kernels sum columns in the same launch, reading their
 // inputs a second time; for the activation's, whose values are also computed twice, up to
-// this many values. Back to back calls, us, one launch against two (3 us of host time each):
-// norm bf16 64 x 7168 7.7, 10.3; 256 x 7168 7.6, 11.4; 512 x 2048 fp32 10.0, 9.8; gelu
-// 64 x 18432 7.0, 9.7; 130 x 18432 11.3, 9.7; 256 x 2048 7.1, 9.9.
+// this many values. Us, one launch against two, back to back calls (3 us of host time for each
+// launch) and in a graph:
+//   norm bf16   64 x  7168   7.7, 10.3    4.5,  7.3     gelu  64 x 18432   7.0, 9.7   5.7, 7.8
+//              256 x  7168   7.6, 11.4    6.9, 11.7          130 x 18432  11.3, 9.7  11.7, 9.6
+//              512 x  7168  11.7, 13.4   12.0, 13.7          256 x  2048   7.1, 9.9   7.4, 6.5
+//              256 x   768   7.8, 10.8    8.0,  6.2          256 x   512   7.2, 9.9   7.4, 6.3
+//       fp32  256 x  2048   7.2,  9.9    7.0,  7.0          512 x   512  12.1, 9.8  12.5, 6.3
+//             512 x  2048  10.0,  9.8   10.5,  7.9
+// The bounds follow the calls. They give away 1 to 2 us in a graph at 256 rows of few columns,
+// and as much of either at 512 rows of many.
 constexpr int64_t kDirectRows = 256, kDirectActValues = 3 << 19;
 
 // Workgroups for `rows` steps of work, at most `most`, evened out so that every workgroup
@@ -1460,7 +1467,9 @@ dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dt
   const int resident = norm_chunks(K) == 1 ? 1024 / nt : 1;
   const dim3 grid((unsigned)even_grid(M, kCUs * resident)), block((unsigned)nt);
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    // the next row ahead, where 256 registers hold it (4096 x 18432 bf16: 99.4 us, not ahead 114.1)
+    // the next row ahead, where 256 registers hold it (4096 x 18432 bf16: 99.4 us, not ahead 114.1);
+    // fp32 with four chunks spills 62 or 86 of them all the same (1000 x 24576, three chunks,
+    // 59.1 us, 5.4 TB/s; 1000 x 32768 124, 3.4)
     constexpr bool ahead = c.value <= (xb.value ? 3 : 2);
     hipLaunchKernelGGL((rmsnorm_kernel<xb.value, wb.value, c.value, ahead>), grid, block, 0,
                        (hipStream_t)stream, a);
@@ -1499,7 +1508,9 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
   NormBwdArgs a{dy, dh, h, weight, rstd, dx, part, dweight, M, (int32_t)K, (int32_t)R, (int32_t)G};
   const unsigned grid = (unsigned)(G + (direct ? K / 64 : 0));
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    constexpr bool ahead = c.value <= 2;  // what 256 registers hold
+    // what 256 registers hold, or nearly: fp32 with two chunks ahead spills 6 or 7 of them, three
+    // not ahead 2 or 8, four 82 or 86 (1000 x 24576 84.5 us, 4.65 TB/s; 1000 x 32768 165, 3.2)
+    constexpr bool ahead = c.value <= 2;
     hipLaunchKernelGGL((rmsnorm_backward_kernel<xb.value, wb.value, c.value, ahead>), dim3(grid),
                        dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
   });

@@ -1,7 +1,8 @@
 // norm_kernel.hpp -- RMS norm with the residual's addition and an FP8 output with 1x128
 // scales, its backward pass, and the backward pass of the GEMM's bias + activation epilogue
-// with an FP8 output, for gfx950. All three are bound by HBM: each value is read once and
-// written once, everything in between stays in registers, in fp32.
+// with an FP8 output, for gfx950. All three are bound by HBM: each value is read once (the
+// backward kernels' on few rows twice, see below) and written once, everything in between
+// stays in registers, in fp32.
 //
 // Forward, row m of K values (K % 128 == 0):
 //   s = x + r (r optional, the sum in fp32, not rounded);  h = s rounded to x's type

@@ -1,7 +1,7 @@
 // ring_kernel.hpp -- block-scaled FP8 GEMM with a fused epilogue for few rows or few tiles,
-// gfx950: tiles of up to 64 (or 128) x 64 or 128, a quarter or an eighth of the tile kernel's,
-// so that products of a few hundred rows still give every CU a tile without splitting K, or
-// with partial tiles of 16 or 32 KB instead of 128.
+// gfx950: tiles of up to 64 x 64 or 128, or of 128 x 128: an eighth, a quarter or half of the
+// tile kernel's, so that products of a few hundred rows still give every CU a tile without
+// splitting K, or with partial tiles of 4 to 64 KB instead of 128.
 //
 // Memory-bound: with up to 64 rows every byte of B meets few rows of A, so the kernel has to
 // keep enough bytes of B in flight on every CU, and to ask for them in the right pieces. A

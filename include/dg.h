@@ -297,8 +297,8 @@ dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dt
  * dy, dh, h and dx have type x_dtype; dh (NULL: zero) is the gradient that reaches h
  * along the residual stream, and dx is the gradient of x and of the residual. dx may be
  * dy, dh or h itself, any other overlap may not. Column sums are added in a fixed order
- * (bitwise deterministic for a given shape and choice of dx). Limits, alignment (dweight 16 bytes) and errors as above; M == 0 writes
- * zeros to dweight.
+ * (bitwise deterministic for a given shape and choice of dx). Limits, alignment (dweight
+ * 16 bytes) and errors as above; M == 0 writes zeros to dweight.
  */
 dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
                               const void* weight, int32_t w_dtype, const float* rstd, void* dx,
