@@ -776,7 +776,7 @@ __device__ __forceinline__ void pipe_store(const Problem& p, const TileView& v, 
 // are the same in all rows, so it loads its bias once, and residual, pre and C move as whole
 // 128-byte row segments. All of the residual is loaded before the first pass, one wait for
 // memory per tile. Nothing overlaps the arithmetic of this epilogue: 4096 x 7168 x 2048 takes
-// 84 us plain, 92 with a residual, 100 with gelu and pre, 104 with gelu and FP8 output.
+// 88 us plain, 96 with a residual, 103 with gelu and pre, 112 with gelu and FP8 output.
 // kEpiFp8: a row's 1x128 block is shared by two waves (wn and wn ^ 1), which hold its two
 // 64-column halves. Each keeps its 64 values per lane, the row maxima meet in pipe_rmax
 // behind one barrier, and the codes go out as 8 bytes per lane, 64-byte row segments. No

@@ -12,7 +12,7 @@
 // a pair of blocks keep 2 (D - 1) blocks in flight whatever the registers hold: 96 KB per CU
 // at D = 3, BN = 128.
 // What bounds it: one CU takes in about 42 KB/us (64 x 18432 x 7168, FP8 output: 144 tiles on as
-// many CUs, 28 KB/us of B and 14 of A each, 39.8 us), HBM gives 20 KB/us of B to each of 256
+// many CUs, 28 KB/us of B and 14 of A each, 37.7 us), HBM gives 20 KB/us of B to each of 256
 // (64 x 32768 x 7168: 43.9 us). Splitting K pays while it brings idle CUs in (64 x 16384 x 7168
 // in two halves: 28.5 us).
 // Per pair: wait for this wave's DMAs of it (vmcnt), one barrier (every wave's DMAs of the
