@@ -19,6 +19,11 @@ article, deepseek.csdn.net, section 4.2 "advanced tuning"):
 * ``fp8_gemm_nt_bias_act(a, b, c, a_sf, b_sf, bias, activation, residual)`` and
   ``fp8_gemm_nt_bias_act_fp8(...)`` -> (codes, sf): the dense GEMM with its epilogue;
   ``bias_act_backward_fp8``: the epilogue's gradients
+* ``layernorm_fp8_1x128(x, weight, bias, eps, residual=..., dropout_p=..., rng=...)``: layer
+  norm of residual + dropout(x) -> (A codes, sfA); ``layernorm_backward``: its gradients
+* ``fp8_gemm_nt_gated_fp8(a, b, a_sf, b_sf, bias, activation)`` -> (codes, sf) of
+  h = activation(gate) * up, both projections in one kernel; ``gated_backward_fp8``
+* ``dropout_add(x, p, rng, residual=...)``; ``dropout_backward_fp8``: its gradient as A codes
 
 Operands: ``a``/``b`` are ``torch.float8_e4m3fn`` (``torch.uint8`` holding e4m3fn
 codes is accepted too), ``a_sf``/``b_sf`` ``torch.float32``, ``c`` ``torch.bfloat16``
@@ -112,6 +117,22 @@ lib.dg_fp8_gemm_nt_bias_act_fp8.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32,
                                             _i32, _vp, _i64, _i64, _i64, _vp]
 lib.dg_bias_act_backward_fp8.restype = ctypes.c_int
 lib.dg_bias_act_backward_fp8.argtypes = [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i64, _i64, _vp]
+
+lib.dg_layernorm_fp8_1x128.restype = ctypes.c_int
+lib.dg_layernorm_fp8_1x128.argtypes = [_vp, _vp, _i32, _vp, _vp, _i32, ctypes.c_float, ctypes.c_double,
+                                       _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp]
+lib.dg_layernorm_backward.restype = ctypes.c_int
+lib.dg_layernorm_backward.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                      _vp]
+lib.dg_fp8_gemm_nt_gated_fp8.restype = ctypes.c_int
+lib.dg_fp8_gemm_nt_gated_fp8.argtypes = lib.dg_fp8_gemm_nt_bias_act_fp8.argtypes
+lib.dg_gated_backward_fp8.restype = ctypes.c_int
+lib.dg_gated_backward_fp8.argtypes = lib.dg_bias_act_backward_fp8.argtypes
+lib.dg_dropout_add.restype = ctypes.c_int
+lib.dg_dropout_add.argtypes = [_vp, _vp, _i32, ctypes.c_double, _vp, _i64, _vp, _i64, _vp]
+lib.dg_dropout_backward_fp8.restype = ctypes.c_int
+lib.dg_dropout_backward_fp8.argtypes = [_vp, _i32, ctypes.c_double, _vp, _i64, _vp, _vp, _i32, _vp, _i64,
+                                        _i64, _vp]
 
 lib.dg_release_workspaces.restype = ctypes.c_int
 lib.dg_release_workspaces.argtypes = []
@@ -555,6 +576,142 @@ def bias_act_backward_fp8(dc, pre=None, activation=None, codes=None, sf=None, db
     return codes, sf, dbias
 
 
+def _rng(rng, x: torch.Tensor, index: int):
+    """rng's address: int64 [2] on x's GPU, (seed, offset); None without one."""
+    return None if rng is None else _ptr(rng, "rng", torch.int64, (2,), x, index)
+
+
+def layernorm_fp8_1x128(x, weight, bias=None, eps=1e-5, residual=None, h=None, mean=None, rstd=None,
+                        codes=None, sf=None, ue8m0=False, dropout_p=0.0, rng=None, subsequence=0):
+    """Layer norm of residual + dropout(x) ([M, K] float32 or bfloat16) with weight and bias [K]
+    (of one dtype, bias optional), quantized per 1x128 block: returns (codes [M, K] e4m3fn, sf),
+    the a and a_sf of the GEMM calls (sf as in rmsnorm_fp8_1x128). h, when passed, receives the
+    sum before the norm (it may be x or residual itself), mean and rstd (fp32 [M]) the row's
+    statistics; layernorm_backward takes all three. dropout_p, rng and subsequence as in
+    dropout_add."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    dtype, w_dtype = _float_type(x, "x"), _float_type(weight, "weight")
+    M, K = shape = x.shape
+    dev = _first(x, "x")
+    w = _ptr(weight, "weight", weight.dtype, (K,), x, dev)
+    b = None if bias is None else _ptr(bias, "bias", weight.dtype, (K,), x, dev)
+    r = None if residual is None else _ptr(residual, "residual", x.dtype, shape, x, dev)
+    hp = None if h is None else _ptr(h, "h", x.dtype, shape, x, dev)
+    mu = None if mean is None else _ptr(mean, "mean", torch.float32, (M,), x, dev)
+    rs = None if rstd is None else _ptr(rstd, "rstd", torch.float32, (M,), x, dev)
+    codes, cp, sf, sp, packed = _fp8_outputs(M, K, codes, sf, ue8m0, x, dev)
+    _launch(dev, lib.dg_layernorm_fp8_1x128, x.data_ptr(), r, dtype, w, b, w_dtype, eps, dropout_p,
+            _rng(rng, x, dev), subsequence, hp, mu, rs, cp, sp, packed, M, K)
+    return codes, sf
+
+
+def layernorm_backward(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=None, dbias=None,
+                       need_dbias=True):
+    """Gradients of layernorm_fp8_1x128 (the quantization taken as the identity), from the h,
+    mean and rstd it stored: returns (dx [M, K] of h's dtype, dweight [K] float32, dbias [K]
+    float32, None with need_dbias=False). dh, the gradient that reaches h along the residual
+    stream, is added to dx; dx is the gradient of the sum before the norm (the residual's as it
+    is, x's through dropout) and may be dy, dh or h itself."""
+    if h.dim() != 2:
+        raise ValueError("h must be [M, K]")
+    dtype, w_dtype = _float_type(h, "h"), _float_type(weight, "weight")
+    M, K = shape = h.shape
+    dev = _first(h, "h")
+    g = _ptr(dy, "dy", h.dtype, shape, h, dev)
+    w = _ptr(weight, "weight", weight.dtype, (K,), h, dev)
+    mu = _ptr(mean, "mean", torch.float32, (M,), h, dev)
+    rs = _ptr(rstd, "rstd", torch.float32, (M,), h, dev)
+    r = None if dh is None else _ptr(dh, "dh", h.dtype, shape, h, dev)
+    if dx is None:
+        dx = torch.empty_like(h)
+    if dweight is None:
+        dweight = torch.empty((K,), dtype=torch.float32, device=h.device)
+    if dbias is None and need_dbias:
+        dbias = torch.empty((K,), dtype=torch.float32, device=h.device)
+    db = None if dbias is None else _ptr(dbias, "dbias", torch.float32, (K,), h, dev)
+    _launch(dev, lib.dg_layernorm_backward, g, r, h.data_ptr(), dtype, w, w_dtype, mu, rs,
+            _ptr(dx, "dx", h.dtype, shape, h, dev), _ptr(dweight, "dweight", torch.float32, (K,), h, dev),
+            db, M, K)
+    return dx, dweight, dbias
+
+
+def fp8_gemm_nt_gated_fp8(a, b, a_sf, b_sf, bias=None, activation="silu", pre=None, codes=None, sf=None,
+                          ue8m0=False):
+    """The gated feed-forward product: with z = a x b^T + bias for b [2I, K] (gate rows, then up
+    rows; bias [2I]), h = activation(z[:, :I]) * z[:, I:] quantized per 1x128 block: returns
+    (codes [M, I] e4m3fn, sf), the down projection's a and a_sf (sf as in rmsnorm_fp8_1x128).
+    I % 128 == 0; pre, when passed, receives z (bf16 [M, 2I], for gated_backward_fp8); the other
+    arguments as for fp8_gemm_nt_bias_act_fp8."""
+    M, N, K, dev, ap, bp, sa, packed, sb, bias_ptr, bias_dtype, pre_ptr = \
+        _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
+    if N % 2:
+        raise ValueError("b must be [2I, K]: gate rows, then up rows")
+    codes, cp, sf, sp, sf_packed = _fp8_outputs(M, N // 2, codes, sf, ue8m0, a, dev)
+    _launch(dev, lib.dg_fp8_gemm_nt_gated_fp8, ap, bp, cp, sp, sf_packed, sa, packed, sb, bias_ptr,
+            bias_dtype, _act(activation), pre_ptr, M, N // 2, K)
+    return codes, sf
+
+
+def gated_backward_fp8(dh, pre, activation="silu", codes=None, sf=None, dbias=None, need_dbias=True,
+                       ue8m0=False):
+    """Backward of fp8_gemm_nt_gated_fp8's epilogue: from dh (bf16 [M, I]) and the pre it stored
+    (bf16 [M, 2I]), p = [dh * up * activation'(gate), dh * activation(gate)], returned as (codes
+    [M, 2I], sf, dbias): p quantized per 1x128 block and dbias [2I] float32 = p summed over rows
+    (None with need_dbias=False). The input's gradient is then fp8_gemm_nn(codes, b, da, sf,
+    b_sf.t().contiguous()) with the forward call's b."""
+    if dh.dim() != 2:
+        raise ValueError("dh must be [M, I]")
+    M, I = shape = dh.shape
+    dev = _first(dh, "dh")
+    d = _ptr(dh, "dh", torch.bfloat16, shape, dh, dev)
+    z = _ptr(pre, "pre", torch.bfloat16, (M, 2 * I), dh, dev)
+    codes, cp, sf, sp, packed = _fp8_outputs(M, 2 * I, codes, sf, ue8m0, dh, dev)
+    if dbias is None and need_dbias:
+        dbias = torch.empty((2 * I,), dtype=torch.float32, device=dh.device)
+    db = None if dbias is None else _ptr(dbias, "dbias", torch.float32, (2 * I,), dh, dev)
+    _launch(dev, lib.dg_gated_backward_fp8, d, z, _act(activation), cp, sp, packed, db, M, I)
+    return codes, sf, dbias
+
+
+def dropout_add(x, p, rng, subsequence=0, residual=None, out=None):
+    """dropout(x) + residual (float32 or bfloat16 of any shape; residual optional), rounded once.
+    An element is dropped with probability p (to the nearest 2^-16) and otherwise divided by
+    1 - p. The mask depends on the element's index, rng's values (int64 [2] on the GPU: seed,
+    offset; read when the kernel runs) and subsequence, which is added to the offset: a training
+    loop counts the offset up, in a captured graph too, and gives each layer its subsequence. No
+    mask is stored: backward calls name the same values. Returns out, which may be x or residual
+    itself. Without a residual this is dropout's own gradient too."""
+    dtype = _float_type(x, "x")
+    dev = _first(x, "x")
+    r = None if residual is None else _ptr(residual, "residual", x.dtype, x.shape, x, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _launch(dev, lib.dg_dropout_add, x.data_ptr(), r, dtype, p, _rng(rng, x, dev), subsequence,
+            _ptr(out, "out", x.dtype, x.shape, x, dev), x.numel())
+    return out
+
+
+def dropout_backward_fp8(dy, p, rng, subsequence=0, codes=None, sf=None, dbias=None, need_dbias=True,
+                         ue8m0=False):
+    """Gradient of dropout_add or layernorm_fp8_1x128 with respect to x, as the FP8 operand of the
+    projection before it: q = dropout(dy) for dy [M, K] (float32 or bfloat16) and the forward
+    call's p, rng values and subsequence, returned as (codes [M, K], sf, dbias): q quantized per
+    1x128 block and dbias [K] float32 = q summed over rows (None with need_dbias=False)."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be [M, K]")
+    dtype = _float_type(dy, "dy")
+    M, K = dy.shape
+    dev = _first(dy, "dy")
+    codes, cp, sf, sp, packed = _fp8_outputs(M, K, codes, sf, ue8m0, dy, dev)
+    if dbias is None and need_dbias:
+        dbias = torch.empty((K,), dtype=torch.float32, device=dy.device)
+    db = None if dbias is None else _ptr(dbias, "dbias", torch.float32, (K,), dy, dev)
+    _launch(dev, lib.dg_dropout_backward_fp8, dy.data_ptr(), dtype, p, _rng(rng, dy, dev), subsequence, cp, sp,
+            packed, db, M, K)
+    return codes, sf, dbias
+
+
 def release_workspaces() -> None:
     """Free the library's own device buffers (split-K partials and counters, transposed
     operand copies) after the devices holding them go idle. No HIP graph holding a
@@ -575,4 +732,5 @@ def config_names() -> list[str]:
 __all__ = ["config_names", "fp8_gemm_nt", "fp8_gemm_nn", "fp8_gemm_tn", "fp8_gemm_tt", "m_grouped_fp8_gemm_nt_contiguous", "m_grouped_fp8_gemm_nt_masked",
            "m_grouped_fp8_gemm_nt_contiguous_swiglu", "m_grouped_fp8_gemm_nt_masked_swiglu",
            "quantize_fp8_1x128", "rmsnorm_fp8_1x128", "rmsnorm_backward", "fp8_gemm_nt_bias_act",
-           "fp8_gemm_nt_bias_act_fp8", "bias_act_backward_fp8", "ACTIVATIONS", "describe_config", "release_workspaces", "BUILD_ID", "DGError", "lib", "LIB_PATH"]
+           "fp8_gemm_nt_bias_act_fp8", "bias_act_backward_fp8", "layernorm_fp8_1x128", "layernorm_backward",
+           "fp8_gemm_nt_gated_fp8", "gated_backward_fp8", "dropout_add", "dropout_backward_fp8", "ACTIVATIONS", "describe_config", "release_workspaces", "BUILD_ID", "DGError", "lib", "LIB_PATH"]

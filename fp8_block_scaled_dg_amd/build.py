@@ -5,12 +5,14 @@ import hashlib
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libdg.so")
-SOURCES = [os.path.join(CSRC, "dg_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.hip", "dg_block.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".hpp")] + [
     os.path.join(ROOT, "include", "dg.h")]
 # measurement companion (streaming-read calibration kernel), loaded by the benchmark only
@@ -38,11 +40,6 @@ def source_hash() -> str:
     return h.hexdigest()[:16]
 
 
-def command(out: str = LIB_PATH, extra: list[str] | None = None) -> list[str]:
-    return ["hipcc", *HIPCC_FLAGS, f'-DDG_BUILD_ID="{source_hash()}"', *(extra or []), "-o", out,
-            *SOURCES]
-
-
 def _hipcc(cmd: list[str], what: str, verbose: bool) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
@@ -54,10 +51,20 @@ def _hipcc(cmd: list[str], what: str, verbose: bool) -> None:
         sys.stderr.write("\n".join(msgs) + "\n")
 
 
-def build(verbose: bool = False) -> str:
-    _hipcc(command(), "libdg.so", verbose)
-    _hipcc(["hipcc", *HIPCC_FLAGS, "-o", PROBE_LIB_PATH, *PROBE_SOURCES], "libdg_probe.so", verbose)
-    return LIB_PATH
+def build(verbose: bool = False, out: str = LIB_PATH, extra: list[str] | None = None) -> str:
+    """Compiles the translation units of libdg.so and the probe library side by side, then
+    links libdg.so."""
+    with tempfile.TemporaryDirectory(prefix="dg_build_") as tmp:
+        compile_only = [f for f in HIPCC_FLAGS if f != "-shared"]
+        units = [(src, os.path.join(tmp, os.path.basename(src) + ".o")) for src in SOURCES]
+        jobs = [(["hipcc", *compile_only, f'-DDG_BUILD_ID="{source_hash()}"', *(extra or []), "-c", "-o", obj,
+                  src], os.path.basename(src)) for src, obj in units]
+        jobs.append((["hipcc", *HIPCC_FLAGS, "-o", PROBE_LIB_PATH, *PROBE_SOURCES], "libdg_probe.so"))
+        with ThreadPoolExecutor(len(jobs)) as pool:
+            list(pool.map(lambda job: _hipcc(*job, verbose), jobs))
+        _hipcc(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", out, *(obj for _, obj in units)],
+               "libdg.so", verbose)
+    return out
 
 
 if __name__ == "__main__":

@@ -37,9 +37,9 @@ __device__ __forceinline__ float act_bell(float z) {
   return __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
 }
 
-// t P(t) + add = Phi(-z) e^(z^2/2) + add, z = |x|
-__device__ __forceinline__ float act_tail(float z, float add) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.26870056986808777f, z, 1.f));
+// t = 1 / (1 + 0.2687 z) and P(t), whose product is Phi(-z) e^(z^2/2), z = |x|
+__device__ __forceinline__ float act_tail_poly(float z, float& t) {
+  t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.26870056986808777f, z, 1.f));
   float p = 0.02952457405626774f;
   p = __builtin_fmaf(p, t, -0.1313483715057373f);
   p = __builtin_fmaf(p, t, 0.1823785901069641f);
@@ -48,7 +48,13 @@ __device__ __forceinline__ float act_tail(float z, float add) {
   p = __builtin_fmaf(p, t, 0.06914930045604706f);
   p = __builtin_fmaf(p, t, 0.1020011231303215f);
   p = __builtin_fmaf(p, t, 0.1069524958729744f);
-  p = __builtin_fmaf(p, t, 0.10720593482255936f);
+  return __builtin_fmaf(p, t, 0.10720593482255936f);
+}
+
+// t P(t) + add
+__device__ __forceinline__ float act_tail(float z, float add) {
+  float t;
+  const float p = act_tail_poly(z, t);
   return __builtin_fmaf(p, t, add);
 }
 
@@ -105,6 +111,47 @@ __device__ __forceinline__ void act_backward(float (&d)[N], const float (&x)[N],
       const float du = __builtin_fmaf(0.134145f * x[i], t * x[i], t);
       d[i] *= __builtin_fmaf(1.5957691216057308f, du, s);
     }
+  }
+}
+
+// Backward of h = act(g) u: (d, g, u) -> (g, u) = (d u act'(g), d act(g)). Value and slope of
+// an activation share their exponential, reciprocal and polynomial.
+template <int N>
+__device__ __forceinline__ void gated_backward(const float (&d)[N], float (&g)[N], float (&u)[N],
+                                               int act) {
+  auto finish = [&](int i, float value, float slope) {
+    g[i] = d[i] * u[i] * slope;
+    u[i] = d[i] * value;
+  };
+  if (act == DG_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) finish(i, g[i] <= 0.f ? 0.f : g[i], g[i] <= 0.f ? 0.f : 1.f);
+  } else if (act == DG_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = act_sigmoid(g[i]), v = g[i] * s;
+      finish(i, v, __builtin_fmaf(v, 1.f - s, s));
+    }
+  } else if (act == DG_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float z = fabsf(g[i]), bell = act_bell(z);
+      float t;
+      const float p = act_tail_poly(z, t);
+      const float q = p * t * bell, s = __builtin_fmaf(p, t, -0.3989422804014327f * z) * bell;
+      finish(i, g[i] * (g[i] > 0.f ? 1.f - q : q), g[i] > 0.f ? 1.f - s : s);
+    }
+  } else if (act == DG_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = act_sigmoid(act_gelu_tanh_u(g[i])), v = g[i] * s;
+      const float t = v * (1.f - s);  // before g^2, as in act_backward
+      const float du = __builtin_fmaf(0.134145f * g[i], t * g[i], t);
+      finish(i, v, __builtin_fmaf(1.5957691216057308f, du, s));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) finish(i, g[i], 1.f);
   }
 }
 

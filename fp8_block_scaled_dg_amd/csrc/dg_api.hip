@@ -26,6 +26,7 @@
 #include "../../include/dg.h"
 #include "epilogue.hpp"
 #include "gemm_kernel.hpp"
+#include "host.hpp"
 #include "norm_kernel.hpp"
 #include "pipe_kernel.hpp"
 #include "quant_kernel.hpp"
@@ -35,7 +36,6 @@
 #include "transpose_kernel.hpp"
 
 namespace dg {
-namespace {
 
 thread_local char g_detail[512] = "";
 
@@ -47,9 +47,9 @@ dg_status fail(dg_status s, const char* fmt, ...) {
   return s;
 }
 
-// ---------------------------------------------------------------- config table
+namespace {
 
-constexpr int64_t kCUs = 256;  // MI355X compute units (8 XCDs x 32)
+// ---------------------------------------------------------------- config table
 
 using Cfg128 = TileCfg<128, 128, 2, 2>;
 using Cfg64 = TileCfg<64, 64, 2, 2>;
@@ -75,29 +75,6 @@ dg_status launch_tile(const Problem& p0, int64_t blocks, hipStream_t stream) {
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
   return DG_OK;
-}
-
-dg_status get_workspace(hipStream_t stream, size_t partial_bytes, size_t counters,
-                        float** partials, uint32_t** counter_ptr);
-
-// Dense tail balancing: with T tiles on kCUs CUs (one workgroup each), the last
-// r = T mod kCUs tiles would run in a partial round. Each of them is split into
-// `parts` K ranges (at least 8 K-blocks each) so that the last round fills the GPU.
-struct TailSplit {
-  int64_t full, parts;
-};
-
-TailSplit pipe_tail_split(int64_t tiles, int64_t KB) {
-  TailSplit t{tiles, 1};
-  const int64_t r = tiles % kCUs;
-  if (r == 0) return t;
-  int64_t parts = kCUs / r;
-  if (parts > 8) parts = 8;
-  if (parts > KB / 8) parts = KB / 8;
-  if (parts < 2) return t;
-  t.full = tiles - r;
-  t.parts = parts;
-  return t;
 }
 
 template <class Cfg, int KIND, int LAY, int EPI>
@@ -143,7 +120,6 @@ dg_status launch_pipe(const Problem& p, int64_t blocks, hipStream_t stream) {
 using Pipe256x128 = PipeCfg<256, 128>;
 using Pipe128x256 = PipeCfg<128, 256>;
 using Pipe128x256L = PipeCfg<128, 256, 12>;  // long K: scales loaded per 12 K-blocks
-constexpr int kLongKB = 32;                  // K-blocks from which the 128x256 tiles use it
 
 // The 128x256-tile kernel, with the scale loads of its K length.
 template <int KIND, int LAY = 0>
@@ -291,6 +267,8 @@ dg_status scratch_workspace(size_t partial_bytes, size_t counters, float** parti
   return DG_OK;
 }
 
+}  // namespace
+
 dg_status get_workspace(hipStream_t stream, size_t partial_bytes, size_t counters,
                         float** partials, uint32_t** counter_ptr) {
   if (g_noalloc) return scratch_workspace(partial_bytes, counters, partials, counter_ptr);
@@ -307,6 +285,8 @@ dg_status get_workspace(hipStream_t stream, size_t partial_bytes, size_t counter
   *counter_ptr = w.counters;
   return DG_OK;
 }
+
+namespace {
 
 // The per-(device, stream) buffers for K-contiguous copies of A (a_bytes) and B.
 dg_status get_transpose_workspace(hipStream_t stream, size_t a_bytes, size_t b_bytes,
@@ -632,10 +612,6 @@ dg_status launch_pipe128_epi(const Problem& p, const Epilogue& ep, hipStream_t s
                                   : launch_pipe_epi<Pipe128x256, EPI>(p, ep, stream);
 }
 
-// The pipelined kernel addresses a tile's rows with 32-bit offsets below 256 * K
-// bytes; this bound keeps them under 2^31.
-constexpr int kPipeMaxKB = (1 << 22) / kKBlock;
-
 const CfgEntry kTable[] = {
     {"tile128x128_w2x2", launch_tile<Cfg128, kDense>, launch_tile<Cfg128, kContiguous>,
      launch_tile<Cfg128, kMasked>, 0, 0},
@@ -812,7 +788,7 @@ dg_status launch(int kind, int id, const Problem& p, int64_t blocks, hipStream_t
 
 // ---------------------------------------------------------------- validation
 
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+}  // namespace
 
 dg_status check_common(const void* A, const void* B, const void* C, const void* sfA,
                        const float* sfB, int64_t N, int64_t K, bool any_output) {
@@ -832,7 +808,6 @@ dg_status check_common(const void* A, const void* B, const void* C, const void* 
   return DG_OK;
 }
 
-}  // namespace
 }  // namespace dg
 
 using namespace dg;
@@ -1253,23 +1228,7 @@ dg_status dg_describe_config(int32_t kind, int64_t M, int64_t N, int64_t K, int3
 namespace dg {
 namespace {
 
-// f(), a C++ exception of the host code (std::bad_alloc of the workspace tables) turned into
-// a status: none leaves a C entry.
-template <class F>
-dg_status no_throw(F f) noexcept {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    return fail(DG_ERR_LAUNCH, "host code: %s", e.what());
-  } catch (...) {
-    return fail(DG_ERR_LAUNCH, "host code: an unknown exception");
-  }
-}
-
 // ---------------------------------------------------------------- GEMM with a fused epilogue
-
-bool known_dtype(int32_t t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
-bool known_act(int32_t a) { return a >= DG_ACT_NONE && a <= DG_ACT_GELU_TANH; }
 
 dg_status gemm_epilogue(const void* A, const void* B, const void* sfA, int32_t sfa_packed,
                         const float* sfB, int64_t M, int64_t N, int64_t K, void* C, bool fp8,
@@ -1309,57 +1268,7 @@ dg_status gemm_epilogue(const void* A, const void* B, const void* sfA, int32_t s
 
 // ---------------------------------------------------------------- norm and its backward
 
-// A row's threads, at most 512, hold 16 values each in one to four chunks. (4096 x 18432,
-// three chunks against two of up to 1024 threads: backward bf16 144 and 160 us, fp32 186 and
-// 262; forward bf16 100 and 90, fp32 92 and 102.)
-int norm_chunks(int64_t K) { return (int)((K + 8191) / 8192); }
-int norm_threads(int64_t K) {
-  const int64_t t = (K / 16 + norm_chunks(K) - 1) / norm_chunks(K);
-  return (int)((t + 63) / 64 * 64);
-}
-
-// Up to this many rows the backward kernels sum columns in the same launch, reading their
-// inputs a second time; for the activation's, whose values are also computed twice, up to
-// this many values. Us, one launch against two, back to back calls (3 us of host time for each
-// launch) and in a graph:
-//   norm bf16   64 x  7168   7.7, 10.3    4.5,  7.3     gelu  64 x 18432   7.0, 9.7   5.7, 7.8
-//              256 x  7168   7.6, 11.4    6.9, 11.7          130 x 18432  11.3, 9.7  11.7, 9.6
-//              512 x  7168  11.7, 13.4   12.0, 13.7          256 x  2048   7.1, 9.9   7.4, 6.5
-//              256 x   768   7.8, 10.8    8.0,  6.2          256 x   512   7.2, 9.9   7.4, 6.3
-//       fp32  256 x  2048   7.2,  9.9    7.0,  7.0          512 x   512  12.1, 9.8  12.5, 6.3
-//             512 x  2048  10.0,  9.8   10.5,  7.9
-// The bounds follow the calls. They give away 1 to 2 us in a graph at 256 rows of few columns,
-// and as much of either at 512 rows of many.
-constexpr int64_t kDirectRows = 256, kDirectActValues = 3 << 19;
-
-// Workgroups for `rows` steps of work, at most `most`, evened out so that every workgroup
-// takes the same number of steps or one fewer (bf16 4096 x 7168 on 512 workgroups, 8 rows
-// each: 34.5 us; on 768, 5 or 6 each: 39.1).
-int64_t even_grid(int64_t rows, int64_t most) {
-  const int64_t each = (rows + most - 1) / most;
-  return (rows + each - 1) / each;
-}
-
-// Calls f with the compile-time form of a norm kernel for these types and K:
-// f(bf16 x?, bf16 weights?, chunks).
-template <class F>
-void norm_form(bool x_bf16, bool w_bf16, int64_t K, F f) {
-  auto by_k = [&](auto xb, auto wb) {
-    using std::integral_constant;
-    switch (norm_chunks(K)) {
-      case 1: f(xb, wb, integral_constant<int, 1>{}); break;
-      case 2: f(xb, wb, integral_constant<int, 2>{}); break;
-      case 3: f(xb, wb, integral_constant<int, 3>{}); break;
-      default: f(xb, wb, integral_constant<int, 4>{}); break;
-    }
-  };
-  auto by_w = [&](auto xb) {
-    if (w_bf16) by_k(xb, std::true_type{});
-    else by_k(xb, std::false_type{});
-  };
-  if (x_bf16) by_w(std::true_type{});
-  else by_w(std::false_type{});
-}
+}  // namespace
 
 dg_status check_rows(int64_t M, int64_t K, const char* k) {
   if (M < 0 || K < 0)
@@ -1399,14 +1308,21 @@ dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N,
   for (int64_t n = 0; n < N; n += kMost) {
     const int64_t cols = N - n < kMost ? N - n : kMost;
     hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, st,
-                       R > 0 ? part + n : part, out + n, (int)R, (int)N);
+                       R > 0 ? part + n : part, out + n, (int)R, (int)N, nullptr, (int)cols);
     const dg_status s = launched("column_sum_kernel");
     if (s != DG_OK) return s;
   }
   return DG_OK;
 }
 
-}  // namespace
+// The same for part[R][2 N], whose halves go to out and out2 (NULL: not wanted). N <= 2^27.
+dg_status launch_column_sum2(const float* part, float* out, float* out2, int64_t R, int64_t N,
+                             hipStream_t st) {
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((out2 ? 2 : 1) * N / 32)), dim3(256), 0, st, part,
+                     out, (int)R, (int)(2 * N), out2, (int)N);
+  return launched("column_sum_kernel");
+}
+
 }  // namespace dg
 
 extern "C" {
@@ -1533,28 +1449,20 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
   if (!aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
   const hipStream_t st = (hipStream_t)stream;
   if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, N, st) : DG_OK;
-  const int64_t strips = (N + 1023) / 1024;
-  // row groups: about 8 workgroups per CU (gelu with its column sums, 4096 x 18432: 78.8 us,
-  // with 16 80.1), of at least 8 rows, two per wave, or 4 where 8 would leave CUs idle
-  // (at least 4 / 8 / 16: 4096 x 2048 19.9 / 16.9 / 16.2 us, 1000 x 512 6.7 / 7.8 / 10.1)
-  const int64_t least = (M + 7) / 8 * strips < kCUs ? 4 : 8;
-  int64_t groups = (8 * kCUs + strips - 1) / strips;
-  if (groups > (M + least - 1) / least) groups = (M + least - 1) / least;
-  const int64_t rows = ((M + groups - 1) / groups + 3) / 4 * 4;
-  groups = (M + rows - 1) / rows;
+  const StripPlan pl = strip_plan(M, N);
   const bool direct = dbias && M <= kDirectRows && M * N <= kDirectActValues, sum = dbias && !direct;
   float* part = nullptr;
   if (sum) {
-    s = get_partials(st, groups * N, &part);
+    s = get_partials(st, pl.groups * N, &part);
     if (s != DG_OK) return s;
   }
   ActBwdArgs a{(const uint16_t*)dc, (const uint16_t*)pre, (uint8_t*)codes,
-               ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)}, part, dbias, M, rows,
-               (int32_t)N, activation, (int32_t)strips, (int32_t)groups};
-  const unsigned grid = (unsigned)(strips * groups + (direct ? N / 64 : 0));
+               ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)}, part, dbias, M, pl.rows,
+               (int32_t)N, activation, (int32_t)pl.strips, (int32_t)pl.groups};
+  const unsigned grid = (unsigned)(pl.strips * pl.groups + (direct ? N / 64 : 0));
   hipLaunchKernelGGL(act_backward_kernel, dim3(grid), dim3(256), 0, st, a);
   s = launched("act_backward_kernel");
-  return s == DG_OK && sum ? launch_column_sum(part, dbias, groups, N, st) : s;
+  return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, N, st) : s;
 }
 
 }  // extern "C"

@@ -1,0 +1,279 @@
+// dg_block.hip -- C ABI of the transformer block's further operators (declared in
+// include/dg.h): layer norm with dropout and FP8 output, the gated feed-forward product,
+// dropout, and their backward passes. Argument checks, choice of a kernel form, launches.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "../../include/dg.h"
+#include "dropout.hpp"
+#include "gated_kernel.hpp"
+#include "host.hpp"
+#include "layernorm_kernel.hpp"
+#include "pipe_kernel.hpp"
+
+namespace dg {
+namespace {
+
+// ---------------------------------------------------------------- dropout
+
+// The device's form of (p, rng, subsequence).
+dg_status drop_args(double p, const int64_t* rng, int64_t subsequence, DropArgs* d) {
+  if (!(p >= 0 && p <= 1)) return fail(DG_ERR_BAD_SHAPE, "dropout_p=%g is not in [0, 1)", p);
+  const uint32_t threshold = (uint32_t)(65536 * p + 0.5);
+  if (threshold > 65535) return fail(DG_ERR_BAD_SHAPE, "dropout_p=%g would keep nothing", p);
+  if (threshold && !rng) return fail(DG_ERR_NULL_POINTER, "NULL rng");
+  if (!aligned(rng, 8)) return fail(DG_ERR_MISALIGNED, "rng must be 8-byte aligned");
+  *d = DropArgs{threshold ? (const uint64_t*)rng : nullptr, (uint64_t)subsequence, threshold,
+                (float)(65536.0 / (65536.0 - threshold))};
+  return DG_OK;
+}
+
+// ---------------------------------------------------------------- gated product
+
+template <class Cfg>
+dg_status launch_pipe_gated(const Problem& p0, const Epilogue& ep, hipStream_t stream) {
+  PipeArgs a{};
+  a.p = p0;
+  a.ep = ep;
+  a.p.tiles_m = (int32_t)((p0.M + Cfg::BM - 1) / Cfg::BM);
+  a.p.tiles_n = (int32_t)(p0.N / 256);
+  int64_t grid = (int64_t)a.p.tiles_m * a.p.tiles_n;
+  if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld tiles", (long long)grid);
+  a.full_tiles = (int32_t)grid;
+  a.parts = 1;
+  const TailSplit ts = pipe_tail_split(grid, p0.K / kKBlock);
+  if (ts.parts > 1) {
+    const int64_t split = grid - ts.full;
+    const size_t bytes = (size_t)(split * ts.parts) * Cfg::BM * Cfg::BN * sizeof(float);
+    const dg_status st = get_workspace(stream, bytes, (size_t)split, &a.ws, &a.counters);
+    if (st != DG_OK) return st;
+    a.full_tiles = (int32_t)ts.full;
+    a.parts = (int32_t)ts.parts;
+    grid = ts.full + split * ts.parts;
+  }
+  a.items = (int32_t)grid;
+  const int64_t wgs = grid < kCUs ? grid : kCUs;  // persistent, one workgroup per CU
+  hipLaunchKernelGGL((pipe_kernel<Cfg, kDense, false, 0, kEpiGated>), dim3((unsigned)wgs), dim3(Cfg::NT),
+                     0, stream, a);
+  return launched("pipe_kernel");
+}
+
+dg_status gated(const Problem& p, const Epilogue& ep, hipStream_t stream) {
+  return p.K / kKBlock >= kLongKB ? launch_pipe_gated<PipeCfg<128, 256, 12>>(p, ep, stream)
+                                  : launch_pipe_gated<PipeCfg<128, 256>>(p, ep, stream);
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dg_status dg_dropout_add(const void* x, const void* residual, int32_t x_dtype, double dropout_p,
+                         const int64_t* rng, int64_t subsequence, void* out, int64_t n,
+                         void* stream) {
+  g_detail[0] = 0;
+  if (!known_dtype(x_dtype))
+    return fail(DG_ERR_BAD_SHAPE, "x_dtype=%d is neither DG_DTYPE_F32 nor DG_DTYPE_BF16", x_dtype);
+  if (n < 0) return fail(DG_ERR_BAD_SHAPE, "negative size n=%lld", (long long)n);
+  DropAddArgs a{x, residual, out, n, {}};
+  const dg_status s = drop_args(dropout_p, rng, subsequence, &a.drop);
+  if (s != DG_OK || n == 0) return s;
+  if (n > (int64_t)1 << 40) return fail(DG_ERR_UNSUPPORTED_SHAPE, "n beyond 2^40");
+  if (!x || !out) return fail(DG_ERR_NULL_POINTER, "NULL x or out");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(out, 16))
+    return fail(DG_ERR_MISALIGNED, "x, residual and out must be 16-byte aligned");
+  const int64_t per_wg = kDropChunk * (kDropThreads / 64) * kDropUnroll;
+  const dim3 grid((unsigned)even_grid((n + per_wg - 1) / per_wg, 8 * kCUs)), block(kDropThreads);
+  if (x_dtype == DG_DTYPE_BF16)
+    hipLaunchKernelGGL(dropout_add_kernel<true>, grid, block, 0, (hipStream_t)stream, a);
+  else
+    hipLaunchKernelGGL(dropout_add_kernel<false>, grid, block, 0, (hipStream_t)stream, a);
+  return launched("dropout_add_kernel");
+}
+
+dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropout_p,
+                                  const int64_t* rng, int64_t subsequence, void* codes, void* sf,
+                                  int32_t sf_packed, float* dbias, int64_t M, int64_t K,
+                                  void* stream) {
+  g_detail[0] = 0;
+  if (!known_dtype(dy_dtype))
+    return fail(DG_ERR_BAD_SHAPE, "dy_dtype=%d is neither DG_DTYPE_F32 nor DG_DTYPE_BF16", dy_dtype);
+  dg_status s = check_rows(M, K, "K");
+  if (s != DG_OK) return s;
+  DropArgs drop;
+  s = drop_args(dropout_p, rng, subsequence, &drop);
+  if (s != DG_OK || K == 0) return s;
+  if (K > (int64_t)1 << 30) return fail(DG_ERR_UNSUPPORTED_SHAPE, "K beyond 2^30");
+  if (M > 0 && (!dy || !codes || !sf)) return fail(DG_ERR_NULL_POINTER, "NULL dy, codes or sf");
+  if (!aligned(dy, 16) || !aligned(codes, 16) || !aligned(dbias, 16))
+    return fail(DG_ERR_MISALIGNED, "dy, codes and dbias must be 16-byte aligned");
+  if (!aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, K, st) : DG_OK;
+  const StripPlan pl = strip_plan(M, K);
+  const bool direct = dbias && M <= kDirectRows && M * K <= kDirectActValues, sum = dbias && !direct;
+  float* part = nullptr;
+  if (sum) {
+    s = get_partials(st, pl.groups * K, &part);
+    if (s != DG_OK) return s;
+  }
+  const DropBwdArgs a{dy, (uint8_t*)codes, ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(K / 128)}, part,
+                      dbias, M, pl.rows, (int32_t)K, (int32_t)pl.strips, (int32_t)pl.groups, drop};
+  const dim3 grid((unsigned)(pl.strips * pl.groups + (direct ? K / 64 : 0)));
+  if (dy_dtype == DG_DTYPE_BF16)
+    hipLaunchKernelGGL(dropout_backward_kernel<true>, grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(dropout_backward_kernel<false>, grid, dim3(256), 0, st, a);
+  s = launched("dropout_backward_kernel");
+  return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, K, st) : s;
+}
+
+dg_status dg_layernorm_fp8_1x128(const void* x, const void* residual, int32_t x_dtype,
+                                 const void* weight, const void* bias, int32_t w_dtype, float eps,
+                                 double dropout_p, const int64_t* rng, int64_t subsequence, void* h,
+                                 float* mean, float* rstd, void* codes, void* sf, int32_t sf_packed,
+                                 int64_t M, int64_t K, void* stream) {
+  g_detail[0] = 0;
+  dg_status s = check_norm(x_dtype, w_dtype, M, K);
+  if (s != DG_OK) return s;
+  if (!(eps > 0.f && eps < INFINITY)) return fail(DG_ERR_BAD_SHAPE, "eps=%g is not positive", (double)eps);
+  LayerNormArgs a{x, residual, weight, bias, h, mean, rstd, (uint8_t*)codes,
+                  ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(K / 128)}, M, (int32_t)K, eps, {}};
+  s = drop_args(dropout_p, rng, subsequence, &a.drop);
+  if (s != DG_OK || M == 0 || K == 0) return s;
+  if (!x || !weight || !codes || !sf) return fail(DG_ERR_NULL_POINTER, "NULL x, weight, codes or sf");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(bias, 16) ||
+      !aligned(h, 16) || !aligned(codes, 16))
+    return fail(DG_ERR_MISALIGNED, "x, residual, weight, bias, h and codes must be 16-byte aligned");
+  if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(sf, 4))
+    return fail(DG_ERR_MISALIGNED, "mean, rstd and sf must be 4-byte aligned");
+  const int nt = norm_threads(K);
+  const int resident = norm_chunks(K) == 1 ? 1024 / nt : 1;  // as for the RMS norm
+  const dim3 grid((unsigned)even_grid(M, kCUs * resident)), block((unsigned)nt);
+  norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
+    constexpr bool ahead = c.value <= (xb.value ? 2 : 1);
+    if (a.drop.threshold)
+      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, ahead, true>), grid, block, 0,
+                         (hipStream_t)stream, a);
+    else
+      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, ahead, false>), grid, block, 0,
+                         (hipStream_t)stream, a);
+  });
+  return launched("layernorm_kernel");
+}
+
+dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
+                                const void* weight, int32_t w_dtype, const float* mean,
+                                const float* rstd, void* dx, float* dweight, float* dbias, int64_t M,
+                                int64_t K, void* stream) {
+  g_detail[0] = 0;
+  dg_status s = check_norm(x_dtype, w_dtype, M, K);
+  if (s != DG_OK || K == 0) return s;
+  if (!dweight || (M > 0 && (!dy || !h || !weight || !mean || !rstd || !dx)))
+    return fail(DG_ERR_NULL_POINTER, "NULL dy, h, weight, mean, rstd, dx or dweight");
+  if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(weight, 16) ||
+      !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(dbias, 16))
+    return fail(DG_ERR_MISALIGNED, "dy, dh, h, weight, dx, dweight and dbias must be 16-byte aligned");
+  if (!aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(DG_ERR_MISALIGNED, "mean and rstd must be 4-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  if (M == 0) return launch_column_sum2(nullptr, dweight, dbias, 0, K, st);
+  // workgroups and teams as for the RMS norm's backward
+  const int nt = norm_threads(K);
+  int64_t R = nt < 512 ? 512 / nt : 1;
+  if (R > (M + kCUs - 1) / kCUs) R = (M + kCUs - 1) / kCUs;
+  const int64_t G = even_grid((M + R - 1) / R, kCUs);
+  // a dx in the place of dy or h would be written while the column sums read them
+  const bool direct = M <= kDirectRows && dx != dy && dx != h;
+  float* part = nullptr;
+  if (!direct) {
+    s = get_partials(st, G * 2 * K, &part);
+    if (s != DG_OK) return s;
+  }
+  const LayerNormBwdArgs a{dy, dh, h, weight, mean, rstd, dx, part, dweight, dbias, M, (int32_t)K,
+                           (int32_t)R, (int32_t)G};
+  const unsigned grid = (unsigned)(G + (direct ? K / 64 : 0));
+  norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
+    constexpr bool ahead = c.value <= (xb.value ? 2 : 1);
+    hipLaunchKernelGGL((layernorm_backward_kernel<xb.value, wb.value, c.value, ahead>), dim3(grid),
+                       dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
+  });
+  s = launched("layernorm_backward_kernel");
+  return s == DG_OK && !direct ? launch_column_sum2(part, dweight, dbias, G, K, st) : s;
+}
+
+dg_status dg_fp8_gemm_nt_gated_fp8(const void* A, const void* B, void* codes, void* sf,
+                                   int32_t sf_packed, const void* sfA, int32_t sfA_packed,
+                                   const float* sfB, const void* bias, int32_t bias_dtype,
+                                   int32_t activation, void* pre, int64_t M, int64_t I, int64_t K,
+                                   void* stream) {
+  g_detail[0] = 0;
+  if (M < 0 || I < 0) return fail(DG_ERR_BAD_SHAPE, "negative size (M=%lld, I=%lld)", (long long)M, (long long)I);
+  if (!known_act(activation)) return fail(DG_ERR_BAD_SHAPE, "activation=%d is unknown", activation);
+  if (bias && !known_dtype(bias_dtype))
+    return fail(DG_ERR_BAD_SHAPE, "bias_dtype=%d is neither DG_DTYPE_F32 nor DG_DTYPE_BF16", bias_dtype);
+  if (I % 128 != 0) return fail(DG_ERR_BAD_SHAPE, "I=%lld is not a multiple of 128", (long long)I);
+  if (I > (int64_t)1 << 29 || M > (int64_t)1 << 30)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "I beyond 2^29 or M beyond 2^30");
+  const dg_status s = check_common(A, B, codes, sfA, sfB, 2 * I, K, M > 0 && I > 0);
+  if (s != DG_OK || M == 0 || I == 0) return s;
+  if (!sf) return fail(DG_ERR_NULL_POINTER, "NULL sf");
+  if (!aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
+  if (!aligned(bias, 16) || !aligned(pre, 16))
+    return fail(DG_ERR_MISALIGNED, "bias and pre must be 16-byte aligned");
+  if (K / kKBlock > kPipeMaxKB || (I + 256) * K >= (int64_t)1 << 31)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "K beyond 2^22, or (I + 256) * K beyond 2^31");
+  Problem p{};
+  p.A = (const uint8_t*)A;
+  p.B = (const uint8_t*)B;
+  p.sfA = (const uint8_t*)sfA;
+  p.sfa_packed = sfA_packed != 0;
+  p.sfB = sfB;
+  p.M = M;
+  p.N = 2 * I;
+  p.K = K;
+  p.G = 1;
+  Epilogue ep{};
+  ep.bias = bias;
+  ep.bias_bf16 = bias_dtype == DG_DTYPE_BF16;
+  ep.act = activation;
+  ep.pre = (uint16_t*)pre;
+  ep.codes = (uint8_t*)codes;
+  ep.so = ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(I / 128)};
+  return no_throw([&] { return gated(p, ep, (hipStream_t)stream); });
+}
+
+dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activation, void* codes,
+                                void* sf, int32_t sf_packed, float* dbias, int64_t M, int64_t I,
+                                void* stream) {
+  g_detail[0] = 0;
+  if (!known_act(activation)) return fail(DG_ERR_BAD_SHAPE, "activation=%d is unknown", activation);
+  dg_status s = check_rows(M, I, "I");
+  if (s != DG_OK || I == 0) return s;
+  if (I > (int64_t)1 << 29) return fail(DG_ERR_UNSUPPORTED_SHAPE, "I beyond 2^29");
+  if (M > 0 && (!dh || !pre || !codes || !sf)) return fail(DG_ERR_NULL_POINTER, "NULL dh, pre, codes or sf");
+  if (!aligned(dh, 16) || !aligned(pre, 16) || !aligned(codes, 16) || !aligned(dbias, 16))
+    return fail(DG_ERR_MISALIGNED, "dh, pre, codes and dbias must be 16-byte aligned");
+  if (!aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
+  const hipStream_t st = (hipStream_t)stream;
+  if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, 2 * I, st) : DG_OK;
+  const StripPlan pl = strip_plan(M, I);
+  const bool direct = dbias && M <= kDirectRows && M * I <= kDirectActValues, sum = dbias && !direct;
+  float* part = nullptr;
+  if (sum) {
+    s = get_partials(st, pl.groups * 2 * I, &part);
+    if (s != DG_OK) return s;
+  }
+  const GatedBwdArgs a{(const uint16_t*)dh, (const uint16_t*)pre, (uint8_t*)codes,
+                       ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(I / 64)}, part, dbias, M, pl.rows,
+                       (int32_t)I, activation, (int32_t)pl.strips, (int32_t)pl.groups};
+  hipLaunchKernelGGL(gated_backward_kernel, dim3((unsigned)(pl.strips * pl.groups + (direct ? I / 64 : 0))),
+                     dim3(256), 0, st, a);
+  s = launched("gated_backward_kernel");
+  return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, 2 * I, st) : s;
+}
+
+}  // extern "C"

@@ -3,6 +3,7 @@
 //   z = acc + bias[n];  pre[m][n] = bf16(z) (optional)
 //   kEpiBf16: C[m][n] = bf16(act(z) + residual[m][n])
 //   kEpiFp8:  codes and scales of act(z), quantized per 1x128 block (quant_kernel.hpp)
+//   kEpiGated: N = 2 I, B = [gate; up]: codes and scales of h[m][i] = act(z[m][i]) z[m][I + i]
 //
 // The GEMM kernels pass their fp32 tile through LDS and hand each lane eight consecutive
 // columns of one row at a time, so that the bias is read once per lane and the residual,
@@ -14,14 +15,14 @@
 
 namespace dg {
 
-enum Epi : int { kEpiNone = 0, kEpiBf16 = 1, kEpiFp8 = 2 };
+enum Epi : int { kEpiNone = 0, kEpiBf16 = 1, kEpiFp8 = 2, kEpiGated = 3 };
 
 struct Epilogue {
   const void* bias;          // [N] bf16 or fp32; NULL: none
   const uint16_t* residual;  // [M][N] bf16; NULL: none (may be C itself)
   uint16_t* pre;             // [M][N] bf16; NULL: not stored
-  uint8_t* codes;            // kEpiFp8: e4m3fn [M][N]
-  ScaleOut so;               // kEpiFp8: scales, so.KB = N / 128
+  uint8_t* codes;            // kEpiFp8: e4m3fn [M][N]; kEpiGated: [M][I]
+  ScaleOut so;               // scales, so.KB = N / 128; kEpiGated: I / 128
   int32_t bias_bf16;
   int32_t act;
 };
@@ -59,6 +60,35 @@ __device__ __forceinline__ void epi_act8(const Epilogue& ep, const float (&b)[8]
   for (int i = 0; i < 8; ++i) v[i] += b[i];
   if (ep.pre) __builtin_nontemporal_store(epi_pack8(v), (v4u*)(ep.pre + off));
   act_apply(v, ep.act);
+}
+
+// The gated product of 8 columns: gate and up values (products, row * N + col and I further on)
+// with their biases, pre stored on the way, and act(gate) up as codes; 16 neighbouring lanes hold
+// a row's 1x128 block kb of h, this one its values from code0 on. Every lane of the 16 calls it.
+__device__ __forceinline__ void epi_gated8(const Epilogue& ep, const float (&bg)[8], const float (&bu)[8],
+                                           int64_t row, int64_t I, int kb, int code0, float (&g)[8],
+                                           float (&u)[8]) {
+  const int64_t off = row * 2 * I + kb * 128 + code0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] += bg[i], u[i] += bu[i];
+  if (ep.pre) {
+    __builtin_nontemporal_store(epi_pack8(g), (v4u*)(ep.pre + off));
+    __builtin_nontemporal_store(epi_pack8(u), (v4u*)(ep.pre + off + I));
+  }
+  act_apply(g, ep.act);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    g[i] *= u[i];
+    m = fmaxf(m, fabsf(g[i]));
+  }
+  m = max8(m);
+  const int e = scale_exp(ep.so, fmaxf(m, dppf<kDppMirror16>(m)));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = ldexpf(g[i], -e);
+  *(uint2*)(ep.codes + row * I + kb * 128 + code0) =
+      make_uint2(quant_e4m3fn_x4(g[0], g[1], g[2], g[3]), quant_e4m3fn_x4(g[4], g[5], g[6], g[7]));
+  if (code0 == 0) store_scale(ep.so, row, kb, e);
 }
 
 // + residual, one rounding, store

@@ -1,0 +1,308 @@
+// layernorm_kernel.hpp -- layer norm of residual + dropout(x) with an FP8 output with 1x128
+// scales, and its backward pass, for gfx950. Bound by HBM like the RMS norm's kernels, whose
+// lanes, chunks and teams (norm_kernel.hpp) they share: each value is read once (the backward
+// kernel's of few rows twice) and written once, what lies between stays in registers, in fp32.
+//
+// Forward, row m of K values (K % 128 == 0):
+//   s = dropout(x) + r (both optional; in fp32, not rounded);  h = s rounded to x's type
+//   mean = sum(s) / K;  rstd = 1 / sqrt(sum((s - mean)^2) / K + eps)
+//   y = (s - mean) rstd w + b (b optional);  codes, scale = y quantized per 1x128 block
+// Backward, with xh = (h - mean) rstd and g = w dy:
+//   dx = rstd (g - mean(g) - xh mean(g xh)) + dh (optional)
+//   dweight = sum over rows of dy xh;  dbias = sum over rows of dy
+//
+// The variance is a sum of squared differences from a mean, never a difference of two large
+// sums: each wave takes its own values' mean and squares about it, without a barrier, and the
+// waves' triples (count, mean, squares) are joined behind the row's one barrier by
+//   squares = sum over waves of squares_w + count_w (mean_w - mean)^2
+// (Chan, Golub, LeVeque, "Updating formulae and a pairwise algorithm for computing sample
+// variances", 1979).
+#pragma once
+
+#include "dropout.hpp"
+#include "norm_kernel.hpp"
+
+namespace dg {
+
+// Sum of v over the wave's 64 lanes, in each of them.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dppf<kDppXor1>(v);
+  v += dppf<kDppXor2>(v);
+  v += dppf<kDppMirror8>(v);
+  v += dppf<kDppMirror16>(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+struct LayerNormArgs {
+  const void* x;
+  const void* r;  // NULL: no residual
+  const void* w;
+  const void* b;  // NULL: no bias
+  void* h;        // NULL: the sum is not stored
+  float* mean;    // NULL: not stored
+  float* rstd;    // NULL: not stored
+  uint8_t* codes;
+  ScaleOut so;
+  int64_t M;
+  int32_t K;
+  float eps;
+  DropArgs drop;
+};
+
+// The rows and chunks of rmsnorm_kernel. AHEAD: weights and bias stay in registers and the
+// next row is loaded before the barrier of this one.
+template <bool BF16, bool WBF, int C, bool AHEAD, bool DROP>
+__global__ void __launch_bounds__(kNormThreads) layernorm_kernel(LayerNormArgs a) {
+  __shared__ float buf[2][2][kNormThreads / 64];
+  __shared__ float counts[kNormThreads / 64];
+  const int K = a.K, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const Drop drop(a.drop);
+  int col[C];
+  Weight16<BF16, WBF> w[C], b[C];
+  Raw16<BF16> x[C], r[C];
+  int live = 0;  // the wave's lanes with values, over its chunks
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    col[c] = norm_col<BF16>(c, blockDim.x, threadIdx.x);
+    live += __popcll(__ballot(col[c] < K));
+    if (AHEAD && col[c] < K) {
+      w[c].load(a.w, col[c]);
+      if (a.b) b[c].load(a.b, col[c]);
+    }
+  }
+  const float count = 16.f * (float)live;  // > 0: a row's threads end with a wave that has some
+  if ((threadIdx.x & 63) == 0) counts[wave] = count;
+  auto fetch = [&](int64_t m) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K) {
+        x[c].load(a.x, m * K + col[c]);
+        if (a.r) r[c].load(a.r, m * K + col[c]);
+      }
+  };
+  int64_t m = blockIdx.x;
+  if (AHEAD && m < a.M) fetch(m);
+  for (int par = 0; m < a.M; m += gridDim.x, par ^= 1) {
+    if (!AHEAD) fetch(m);
+    float v[C][16];
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (col[c] >= K) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[c][i] = x[c][i];
+      if (DROP) drop16<BF16>(drop, m * K + col[c], v[c]);
+      if (a.r) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[c][i] += r[c][i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum += v[c][i];
+    }
+    if (AHEAD && m + gridDim.x < a.M) fetch(m + gridDim.x);
+    sum = wave_sum(sum);
+    const float own = sum / count;
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (col[c] >= K) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float d = v[c][i] - own;
+        sq = __builtin_fmaf(d, d, sq);
+      }
+    }
+    sq = wave_sum(sq);
+    if ((threadIdx.x & 63) == 0) buf[par][0][wave] = own, buf[par][1][wave] = sq;
+    lds_barrier();
+    float mean = 0.f, var = 0.f;
+    for (int i = 0; i < waves; ++i) mean = __builtin_fmaf(counts[i], buf[par][0][i], mean);
+    mean /= (float)K;
+    for (int i = 0; i < waves; ++i) {
+      const float d = buf[par][0][i] - mean;
+      var += __builtin_fmaf(counts[i] * d, d, buf[par][1][i]);
+    }
+    const float rstd = 1.f / sqrtf(var / (float)K + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[m] = mean;
+      if (a.rstd) a.rstd[m] = rstd;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (col[c] >= K) continue;
+      if (a.h) store16<BF16>(a.h, m * K + col[c], v[c]);
+      if (!AHEAD) {
+        w[c].load(a.w, col[c]);
+        if (a.b) b[c].load(a.b, col[c]);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[c][i] = (v[c][i] - mean) * rstd * w[c][i];
+      if (a.b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[c][i] += b[c][i];
+      }
+      quantize16<BF16>(v[c], threadIdx.x & 7, m, col[c] >> 7, a.codes, a.so);
+    }
+  }
+}
+
+struct LayerNormBwdArgs {
+  const void* dy;
+  const void* dh;  // NULL: nothing is added to dx
+  const void* h;
+  const void* w;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  float* part;     // [groups][2 K] partial dweight, dbias; NULL: workgroups from `groups` on sum them
+  float* dweight;  // part == NULL: the sums
+  float* dbias;
+  int64_t M;
+  int32_t K;
+  int32_t teams;   // rows that a workgroup works on side by side
+  int32_t groups;  // workgroups that take rows
+};
+
+// The teams and chunks of rmsnorm_backward_kernel, with two sums per row and two per column.
+template <bool BF16, bool WBF, int C, bool AHEAD>
+__global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerNormBwdArgs a) {
+  __shared__ float buf[2][2][kNormThreads / 64];
+  extern __shared__ float teams_sums[];  // [teams - 1][K]
+  const int K = a.K, R = a.teams, threads = blockDim.x / R;
+  if ((int)blockIdx.x >= a.groups) {
+    constexpr int P = Pieces<BF16>::P;
+    direct_column_sums2<P, kNormThreads>(
+        a.M, ((int)blockIdx.x - a.groups) * 64, a.dweight, a.dbias,
+        [&](int64_t m, int c, float (&v)[P], float (&u)[P]) {
+          float d[P], x[P];
+          load_piece<BF16>(a.dy, m * K + c, d);
+          load_piece<BF16>(a.h, m * K + c, x);
+          const float mean = a.mean[m], rstd = a.rstd[m];
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            v[i] = __builtin_fmaf(d[i], (x[i] - mean) * rstd, v[i]);
+            u[i] += d[i];
+          }
+        });
+    return;
+  }
+  const int team = threadIdx.x / threads, t = threadIdx.x - team * threads;
+  const int wave = t >> 6, waves = threads >> 6;
+  int col[C];
+  Weight16<BF16, WBF> w[C];
+  float dw[C][16], db[C][16];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    col[c] = norm_col<BF16>(c, threads, t);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dw[c][i] = db[c][i] = 0.f;
+    if (AHEAD && col[c] < K) w[c].load(a.w, col[c]);
+  }
+  Raw16<BF16> h[C], dy[C], dh[C];
+  float mu = 0.f, rs = 0.f;
+  auto fetch = [&](int64_t m) {
+    mu = a.mean[m];
+    rs = a.rstd[m];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K) {
+        h[c].load(a.h, m * K + col[c]);
+        dy[c].load(a.dy, m * K + col[c]);
+      }
+  };
+  auto fetch_dh = [&](int64_t m) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K && a.dh) dh[c].load(a.dh, m * K + col[c]);
+  };
+  const int64_t step = (int64_t)a.groups * R;
+  int64_t m = (int64_t)blockIdx.x * R + team;
+  if (AHEAD && m < a.M) {
+    fetch(m);
+    fetch_dh(m);
+  }
+  // every team passes every barrier: the loop runs while team 0 has a row
+  for (int par = 0; m - team < a.M; m += step, par ^= 1) {
+    const bool live = m < a.M;
+    if (!AHEAD && live) fetch(m);
+    const float mean = mu, rstd = rs;
+    float xh[AHEAD ? C : 1][16], g[AHEAD ? C : 1][16];
+    float sum = 0.f, dot = 0.f;
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (col[c] >= K) continue;
+        if (!AHEAD) w[c].load(a.w, col[c]);
+        const int k = AHEAD ? c : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float d = dy[c][i];
+          xh[k][i] = (h[c][i] - mean) * rstd;
+          dw[c][i] = __builtin_fmaf(d, xh[k][i], dw[c][i]);
+          db[c][i] += d;
+          g[k][i] = d * w[c][i];
+          sum += g[k][i];
+          dot = __builtin_fmaf(g[k][i], xh[k][i], dot);
+        }
+      }
+    }
+    if (AHEAD && m + step < a.M) fetch(m + step);
+    sum = wave_sum(sum);
+    dot = wave_sum(dot);
+    if ((threadIdx.x & 63) == 0) {
+      buf[par][0][team * waves + wave] = sum;
+      buf[par][1][team * waves + wave] = dot;
+    }
+    lds_barrier();
+    sum = dot = 0.f;
+    for (int i = 0; i < waves; ++i) sum += buf[par][0][team * waves + i], dot += buf[par][1][team * waves + i];
+    sum /= (float)K;
+    dot /= (float)K;
+    if (live) {
+      if (!AHEAD) fetch_dh(m);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (col[c] >= K) continue;
+        const int k = AHEAD ? c : 0;
+        if (!AHEAD) {
+          w[c].load(a.w, col[c]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) xh[k][i] = (h[c][i] - mean) * rstd, g[k][i] = dy[c][i] * w[c][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          g[k][i] = rstd * __builtin_fmaf(-xh[k][i], dot, g[k][i] - sum);
+          if (a.dh) g[k][i] += dh[c][i];
+        }
+        store16<BF16>(a.dx, m * K + col[c], g[k]);
+      }
+    }
+    if (AHEAD && m + step < a.M) fetch_dh(m + step);
+  }
+  if (!a.part) return;
+  // one sum after the other through the same LDS; every team passes every barrier
+#pragma unroll
+  for (int k = 0; k < 2 && R > 1; ++k) {
+    float(&own)[C][16] = k ? db : dw;
+    if (k) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (team > 0 && col[c] < K) store_sums16<BF16>(teams_sums + (team - 1) * K + col[c], own[c]);
+    __syncthreads();
+    for (int q = 0; q < R - 1 && team == 0; ++q)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (col[c] < K) add_sums16<BF16>(teams_sums + q * K + col[c], own[c]);
+  }
+  if (team > 0) return;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * K;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (col[c] < K) {
+      store_sums16<BF16>(part + col[c], dw[c]);
+      store_sums16<BF16>(part + K + col[c], db[c]);
+    }
+}
+
+}  // namespace dg

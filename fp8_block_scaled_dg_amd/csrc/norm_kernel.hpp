@@ -244,6 +244,27 @@ __device__ __forceinline__ void direct_column_sums(int64_t M, int col0, float* o
   }
 }
 
+// The same for two sums per column: add(m, col, v, u). out_u may be NULL: only v's are stored.
+template <int P, int NT, class F>
+__device__ __forceinline__ void direct_column_sums2(int64_t M, int col0, float* out_v, float* out_u,
+                                                    F add) {
+  constexpr int L = 64 / P;
+  __shared__ float sums[2][NT / L][64];
+  const int groups = blockDim.x / L, r = threadIdx.x / L, c = (threadIdx.x % L) * P;
+  float v[P], u[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) v[i] = u[i] = 0.f;
+  for (int64_t m = r; m < M; m += groups) add(m, col0 + c, v, u);
+#pragma unroll
+  for (int i = 0; i < P; ++i) sums[0][r][c + i] = v[i], sums[1][r][c + i] = u[i];
+  __syncthreads();
+  for (int k = threadIdx.x; k < (out_u ? 128 : 64); k += blockDim.x) {
+    float s = 0.f;
+    for (int i = 0; i < groups; ++i) s += sums[k >> 6][i][k & 63];
+    (k < 64 ? out_v : out_u)[col0 + (k & 63)] = s;
+  }
+}
+
 // P consecutive values of a bf16 (P = 8) or fp32 (P = 4) array, 16 bytes.
 template <bool BF16>
 __device__ __forceinline__ void load_piece(const void* src, int64_t idx, float (&v)[Pieces<BF16>::P]) {
@@ -507,7 +528,7 @@ struct ActBwdArgs {
 // A workgroup of four waves takes a strip of 1024 columns (8 blocks of 128, 8 lanes each)
 // over a group of rows, wave w rows w, w + 4, ... of the group, the next row's loads in
 // flight; the waves' column sums meet in LDS.
-__global__ void __launch_bounds__(256) act_backward_kernel(ActBwdArgs a) {
+static __global__ void __launch_bounds__(256) act_backward_kernel(ActBwdArgs a) {
   __shared__ float sums[3][1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int)blockIdx.x >= a.strips * a.groups) {
@@ -561,11 +582,12 @@ __global__ void __launch_bounds__(256) act_backward_kernel(ActBwdArgs a) {
   store_sums16<true>(a.part + (int64_t)group * a.N + col, sum);
 }
 
-// out[n] = sum of the R partial rows part[.][n], n < N (N % 32 == 0): a workgroup takes 32
-// columns (a 128-byte line of each row), thread (q, r) rows r, r + 32, ... of columns
-// 4q .. 4q+3 with eight loads in flight (past the last row: the last row again, not added),
-// and the 32 row sums are added pairwise in LDS.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, float* out, int R, int N) {
+// out[n] = sum of the R partial rows part[.][n], `pitch` values apart, and from column `split`
+// on out2[n - split] (split % 32 == 0): a workgroup takes 32 columns (a 128-byte line of each
+// row), thread (q, r) rows r, r + 32, ... of columns 4q .. 4q+3 with eight loads in flight (past
+// the last row: the last row again, not added), and the 32 row sums are added pairwise in LDS.
+static __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, float* out, int R,
+                                                                int pitch, float* out2, int split) {
   __shared__ nk_v4f s[32][8];
   constexpr int U = 8;
   const int q = threadIdx.x & 7, r = threadIdx.x >> 3;
@@ -574,7 +596,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, floa
   for (int i = r; i < R; i += 32 * U) {
     nk_v4f v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = *(const nk_v4f*)(part + (int64_t)min(i + 32 * u, R - 1) * N + col);
+    for (int u = 0; u < U; ++u) v[u] = *(const nk_v4f*)(part + (int64_t)min(i + 32 * u, R - 1) * pitch + col);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -590,7 +612,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, floa
       s[r][q] = sum;
     }
   }
-  if (r == 0) *(nk_v4f*)(out + col) = sum;
+  if (r == 0) *(nk_v4f*)(col < split ? out + col : out2 + (col - split)) = sum;
 }
 
 }  // namespace dg

@@ -877,6 +877,76 @@ __device__ __forceinline__ void pipe_store_epi(const Problem& p, const TileView&
   }
 }
 
+// The gated product's epilogue (kEpiGated; BM = 128, BN = 256: tile columns 0..127 are gate
+// columns n0.., 128..255 the up columns I + n0..). The waves put their fp32 sub-tiles into LDS,
+// 1 KB a row, all 128 KB of them in the three stages; behind one barrier each wave takes 16 whole
+// rows back, 16 lanes to a row with 8 gate and 8 up columns each, so that a lane meets its biases
+// once, a row's 1x128 block of h is reduced by lane moves, and pre and the codes go out as whole
+// lines. 16-byte chunk c of a row's half sits at chunk (c / 2 + 16 (c % 2)) ^ (row % 32), which
+// lets 16 lanes reading their even (odd) chunks hit disjoint banks, and the writes too.
+__device__ __forceinline__ uint8_t* pipe_gated_row(int row) {  // 48 rows a stage
+  return row < 48 ? pipe_stage0 + row * 1024
+                  : row < 96 ? pipe_stage1 + (row - 48) * 1024 : pipe_stage2 + (row - 96) * 1024;
+}
+
+template <class Cfg>
+__device__ __forceinline__ void pipe_store_gated(const Problem& p, const TileView& v,
+                                                 const v16f (&acc)[Cfg::TM][Cfg::TN],
+                                                 const Epilogue& ep) {
+  static_assert(Cfg::BM == 128 && Cfg::BN == 256, "gate and up halves of 128 columns");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  const int r32 = lane & 31, g = lane >> 5;
+  const int64_t I = p.N / 2;
+  const int kb = (int)(v.n0 / 128), l16 = lane & 15;
+  float bg[8], bu[8];
+  epi_bias8(ep, v.n0 + 8 * l16, bg);
+  epi_bias8(ep, I + v.n0 + 8 * l16, bu);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = wm * 64 + i * 32 + r32;
+    uint8_t* dst = pipe_gated_row(row);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // chunk c = 16 (wn % 2) + 8 j + 2 q + g of the half wn / 2
+        const int pos = ((8 * (wn & 1) + 4 * j + q + 16 * g) ^ r32) + 32 * (wn >> 1);
+        const v16f& t = acc[i][j];
+        *(v4f*)(dst + pos * 16) = v4f{t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]};
+      }
+  }
+  lds_barrier();
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int rl = wave * 16 + s * 4 + (lane >> 4);
+    const int64_t row = v.m0 + rl;
+    if (row >= p.M) continue;  // the same for a row's 16 lanes
+    const uint8_t* src = pipe_gated_row(rl);
+    const int c0 = l16 ^ (rl & 31), c1 = (16 + l16) ^ (rl & 31);
+    const v4f g0 = *(const v4f*)(src + c0 * 16), g1 = *(const v4f*)(src + c1 * 16);
+    const v4f u0 = *(const v4f*)(src + 512 + c0 * 16), u1 = *(const v4f*)(src + 512 + c1 * 16);
+    float gate[8], up[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gate[i] = g0[i], gate[4 + i] = g1[i], up[i] = u0[i], up[4 + i] = u1[i];
+    epi_gated8(ep, bg, bu, row, I, kb, 8 * l16, gate, up);
+  }
+  lds_barrier();  // the stages are free for the next tile's DMAs
+}
+
+// The epilogue of form EPI.
+template <class Cfg, int EPI>
+__device__ __forceinline__ void pipe_store_as(const Problem& p, const TileView& v,
+                                              const v16f (&acc)[Cfg::TM][Cfg::TN], const Epilogue& ep) {
+  if constexpr (EPI == kEpiGated)
+    pipe_store_gated<Cfg>(p, v, acc, ep);
+  else if constexpr (EPI != kEpiNone)
+    pipe_store_epi<Cfg, EPI>(p, v, acc, ep);
+  else
+    pipe_store<Cfg, kDense>(p, v, 0, (int)p.M, acc);
+}
+
 // Where the fused SwiGLU epilogue writes: e4m3fn codes [rows][I] and fp32 scales
 // [rows][I/128] of h = silu(gate) * up (rows as in the GEMM's A).
 struct SwigluOut {
@@ -975,6 +1045,12 @@ __device__ __forceinline__ void pipe_store_swiglu(const Problem& p, const TileVi
   __syncthreads();  // the LDS is free again (the contiguous layout may run another pass)
 }
 
+// pipe_mainloop's b_hi of a dense tile.
+template <int EPI>
+__device__ __forceinline__ int pipe_b_hi(const Problem& p) {
+  return EPI == kEpiGated ? (int)(p.N / 2 - 128) : 0;
+}
+
 template <class Cfg, int KIND, bool SWIGLU = false, int LAY = 0, int EPI = kEpiNone>
 __device__ __forceinline__ void pipe_tile(const Problem& p, const TileView& v, int expert,
                                           int valid_rows, uint32_t quarters = ~0u,
@@ -985,9 +1061,9 @@ __device__ __forceinline__ void pipe_tile(const Problem& p, const TileView& v, i
     pipe_mainloop<Cfg>(p, v, 0, (int)(p.K / kKBlock), acc, quarters, sw.I - 128);
     pipe_store_swiglu<Cfg, KIND>(p, v, expert, valid_rows, acc, sw);
   } else {
-    pipe_mainloop<Cfg, LAY>(p, v, 0, (int)(p.K / kKBlock), acc, quarters);
+    pipe_mainloop<Cfg, LAY>(p, v, 0, (int)(p.K / kKBlock), acc, quarters, pipe_b_hi<EPI>(p));
     if constexpr (EPI != kEpiNone)
-      pipe_store_epi<Cfg, EPI>(p, v, acc, ep);
+      pipe_store_as<Cfg, EPI>(p, v, acc, ep);
     else
       pipe_store<Cfg, KIND>(p, v, expert, valid_rows, acc);
   }
@@ -1069,7 +1145,7 @@ __device__ __forceinline__ void pipe_split_tile(const PipeArgs& a, const TileVie
                                                 int part, int kb_lo, int kb_hi) {
   constexpr int TM = Cfg::TM, TN = Cfg::TN, BMN = Cfg::BM * Cfg::BN;
   v16f acc[TM][TN];
-  pipe_mainloop<Cfg, LAY>(a.p, v, kb_lo, kb_hi, acc);
+  pipe_mainloop<Cfg, LAY>(a.p, v, kb_lo, kb_hi, acc, ~0u, pipe_b_hi<EPI>(a.p));
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(
       a.ws + (int64_t)tt * a.parts * BMN, 0, 0x7FFFFFFF, 0x00020000);
@@ -1124,23 +1200,22 @@ __device__ __forceinline__ void pipe_split_tile(const PipeArgs& a, const TileVie
   }
   if (tid == 0)
     __hip_atomic_store(&a.counters[tt], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if constexpr (EPI != kEpiNone)
-    pipe_store_epi<Cfg, EPI>(a.p, v, sum, a.ep);
-  else
-    pipe_store<Cfg, kDense>(a.p, v, 0, (int)a.p.M, sum);
+  pipe_store_as<Cfg, EPI>(a.p, v, sum, a.ep);
 }
 
 // One work item: a tile (or, dense, a K part of a tail tile). `item` plays the role
 // of the workgroup index in the tile order: item i runs on XCD i % 8.
 // SWIGLU (grouped layouts, 128x256 tiles): B is [gate; up] with 2 * sw.I rows per
 // expert, tile tn covers gate columns 128 tn.. and the matching up columns, and the
-// fused epilogue writes quantized h instead of bf16 C.
+// fused epilogue writes quantized h instead of bf16 C. EPI = kEpiGated: the same tiles of a
+// dense product, with its own epilogue.
 template <class Cfg, int KIND, bool SWIGLU, int LAY, int EPI>
 __device__ __forceinline__ void pipe_item(const PipeArgs& args, int item) {
   static_assert(LAY == 0 || (KIND == kDense && !SWIGLU), "other layouts: dense GEMM only");
   static_assert(EPI == kEpiNone || KIND == kDense, "bias and activation: dense GEMM only");
   static_assert(!SWIGLU || KIND != kDense, "the fused epilogue is for the grouped layouts");
-  constexpr int NSTEP = SWIGLU ? 128 : Cfg::BN;  // columns between consecutive N-tiles
+  // columns between consecutive N-tiles
+  constexpr int NSTEP = SWIGLU || EPI == kEpiGated ? 128 : Cfg::BN;
   const Problem& p = args.p;
   if (KIND == kDense && item >= args.full_tiles) {
     const int h = item - args.full_tiles;
@@ -1150,7 +1225,7 @@ __device__ __forceinline__ void pipe_item(const PipeArgs& args, int item) {
     const int KB = (int)(p.K / kKBlock);
     TileView v;
     v.m0 = (int64_t)tm * Cfg::BM;
-    v.n0 = (int64_t)tn * Cfg::BN;
+    v.n0 = (int64_t)tn * NSTEP;
     v.A = p.A;
     v.sfA = p.sfA;
     v.C = p.C;

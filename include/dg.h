@@ -75,8 +75,9 @@ typedef enum dg_status {
   DG_OK = 0,
   DG_ERR_NULL_POINTER = 1,      /* a required pointer is NULL                    */
   DG_ERR_BAD_SHAPE = 2,         /* negative size, K % 128 != 0, N % 16 != 0, G<1, */
-                                /* an unknown dg_dtype or dg_activation, or an    */
-                                /* eps that is not positive and finite            */
+                                /* an unknown dg_dtype or dg_activation, an eps   */
+                                /* that is not positive and finite, or a dropout  */
+                                /* probability out of range                       */
   DG_ERR_UNSUPPORTED_SHAPE = 3, /* valid but beyond what the kernels index       */
   DG_ERR_MISALIGNED = 4,        /* A/B/C not 16-byte or scales not 4-byte aligned */
   DG_ERR_NO_DEVICE = 5,         /* no usable gfx950 device                       */
@@ -362,6 +363,118 @@ dg_status dg_fp8_gemm_nt_bias_act_fp8(const void* A, const void* B, void* codes,
 dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t activation,
                                    void* codes, void* sf, int32_t sf_packed, float* dbias,
                                    int64_t M, int64_t N, void* hip_stream);
+
+/*
+ * Dropout from a counter-based generator; no mask is stored. With t = round(65536 p) and r_i
+ * the 16 random bits of element i (its row-major index in the tensor):
+ *   dropout(x)_i = r_i >= t ? x_i * 65536 / (65536 - t) : 0
+ * r_i is half i % 2 (low first) of word (i % 8) / 2 of a Philox 4x32 block of 7 rounds with
+ * the two words of the seed (low first) as its key and, as its counter, the two words of i / 8
+ * and the two words of offset + subsequence (64 bits, wrapping).
+ *   rng  int64 [2] in device memory: seed, offset, read when the kernel runs, so that a
+ *        captured graph draws new masks when the caller changes them between replays
+ * Calls with the same rng values, subsequence and shape draw the same mask (the backward of a
+ * call names its values again); other offsets or subsequences draw independent ones.
+ * 0 <= p, and p rounds to less than one in 2^-16 steps; with p = 0 rng may be NULL. A dropped
+ * NaN or infinity is 0.
+ */
+
+/*
+ * out = dropout(x) + residual, n values of one type (x_dtype), rounded once. residual: NULL for
+ * none. out may be x or residual itself, any other overlap may not. Without a residual this is
+ * dropout's own gradient too. Any n <= 2^40; x, residual and out 16-byte aligned, rng 8-byte.
+ * n == 0 returns DG_OK and launches nothing.
+ */
+dg_status dg_dropout_add(const void* x, const void* residual, int32_t x_dtype, double dropout_p,
+                         const int64_t* rng, int64_t subsequence, void* out, int64_t n,
+                         void* hip_stream);
+
+/*
+ * Backward of dropout into the FP8 operand of the projection before it: with p = dropout(dy)
+ * (dy [M][K] of type dy_dtype, as one tensor),
+ *   codes, sf = p quantized as dg_quantize_fp8_1x128 quantizes (sf_packed as in
+ *     dg_rmsnorm_fp8_1x128): the A operand of dg_fp8_gemm_nn, as in dg_bias_act_backward_fp8
+ *   dbias  fp32 [K] = sum_m p (before quantization; NULL: not computed)
+ * K % 128 == 0, K <= 2^30, M * K <= 2^40; dy, codes and dbias 16-byte aligned, sf 4-byte. Column
+ * sums are added in a fixed order. M == 0 writes zeros to dbias. Codes and scales of a block
+ * holding an infinity or NaN are unspecified.
+ */
+dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropout_p,
+                                  const int64_t* rng, int64_t subsequence, void* codes, void* sf,
+                                  int32_t sf_packed, float* dbias, int64_t M, int64_t K,
+                                  void* hip_stream);
+
+/*
+ * Layer norm of residual + dropout(x) with an FP8 output, the counterpart of
+ * dg_rmsnorm_fp8_1x128:
+ *   s = dropout(x) + residual (in fp32, not rounded; dropout_p = 0: x + residual)
+ *   mean[m] = sum_k s / K;  rstd[m] = 1 / sqrt(sum_k (s - mean)^2 / K + eps)
+ *   y = (s - mean) * rstd * weight + bias;  codes, sf = y quantized
+ *   weight, bias  [K], fp32 or bf16 (w_dtype); bias may be NULL (none)
+ *   h [M][K] = s rounded once, mean, rstd fp32 [M]: NULL where not wanted; all three are what
+ *   dg_layernorm_backward takes. h may be x or residual itself, any other overlap may not.
+ * Sums are fp32, the variance a sum of squared differences from a mean. A row that holds a NaN
+ * or an infinity, or whose squares overflow fp32, gives what the formula gives in fp32.
+ * The gradient of s goes to the residual as it is and to x through dropout
+ * (dg_dropout_backward_fp8, dg_dropout_add).
+ * K % 128 == 0, K <= 32768; eps positive and finite; M * K <= 2^40; x, residual, weight, bias, h
+ * and codes 16-byte aligned, mean, rstd and sf 4-byte, rng 8-byte. M == 0 or K == 0 returns DG_OK
+ * and launches nothing.
+ */
+dg_status dg_layernorm_fp8_1x128(const void* x, const void* residual, int32_t x_dtype,
+                                 const void* weight, const void* bias, int32_t w_dtype, float eps,
+                                 double dropout_p, const int64_t* rng, int64_t subsequence, void* h,
+                                 float* mean, float* rstd, void* codes, void* sf, int32_t sf_packed,
+                                 int64_t M, int64_t K, void* hip_stream);
+
+/*
+ * Backward of the layer norm (the quantization taken as the identity): with
+ * xh = (h - mean) * rstd and g = weight * dy,
+ *   dx [M][K] = rstd * (g - mean_k(g) - xh * mean_k(g * xh)) + dh
+ *   dweight fp32 [K] = sum_m dy * xh;  dbias fp32 [K] = sum_m dy (NULL: not computed)
+ * dy, dh, h and dx have type x_dtype; dh (NULL: zero) is the gradient that reaches h along the
+ * residual stream, and dx is the gradient of s. dx may be dy, dh or h itself, any other overlap
+ * may not. Column sums are added in a fixed order (bitwise deterministic for a given shape and
+ * choice of dx). Limits, alignment (dweight and dbias 16 bytes) and errors as above; M == 0
+ * writes zeros to dweight and dbias.
+ */
+dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
+                                const void* weight, int32_t w_dtype, const float* mean,
+                                const float* rstd, void* dx, float* dweight, float* dbias, int64_t M,
+                                int64_t K, void* hip_stream);
+
+/*
+ * The gated feed-forward product: both projections, the activation and the product in one
+ * kernel, with an FP8 output that is the down projection's A and sfA. B holds the gate
+ * projection in rows [0, I) and the up projection in rows [I, 2 I). With z [M][2 I] = the
+ * block-scaled product of dg_fp8_gemm_nt in fp32, before rounding, plus bias:
+ *   h[m][i] = activation(z[m][i]) * z[m][I + i];  codes, sf = h quantized
+ *   sfB   fp32 [2 I / 128][K/128];  bias [2 I] fp32 or bf16 (bias_dtype), NULL: none
+ *   codes e4m3fn [M][I];  sf fp32 [M][I/128] or (sf_packed) uint32 [M][ceil(I/512)]
+ *   pre   bf16 [M][2 I] = z, for dg_gated_backward_fp8; NULL: not stored
+ * I % 128 == 0, K <= 2^22, (I + 256) * K < 2^31; alignment, stream, workspace and error rules of
+ * dg_fp8_gemm_nt_bias_act_fp8. Codes and scales of a block holding an infinity or NaN are
+ * unspecified.
+ */
+dg_status dg_fp8_gemm_nt_gated_fp8(const void* A, const void* B, void* codes, void* sf,
+                                   int32_t sf_packed, const void* sfA, int32_t sfA_packed,
+                                   const float* sfB, const void* bias, int32_t bias_dtype,
+                                   int32_t activation, void* pre, int64_t M, int64_t I, int64_t K,
+                                   void* hip_stream);
+
+/*
+ * Its backward: with zg, zu the halves of pre and dh bf16 [M][I] the gradient of h,
+ *   p [M][2 I] = [dh * zu * activation'(zg), dh * activation(zg)]
+ *   codes e4m3fn [M][2 I], sf = p quantized: the A operand and sfA of
+ *     dg_fp8_gemm_nn(codes, B, dA, sf, sfB^T) with B [2 I][K] as it is stored
+ *   dbias  fp32 [2 I] = sum_m p (before quantization; NULL: not computed)
+ * I % 128 == 0, I <= 2^29, M * I <= 2^40; dh, pre, codes and dbias 16-byte aligned, sf 4-byte.
+ * Column sums are added in a fixed order. M == 0 writes zeros to dbias. Codes and scales of a
+ * block holding an infinity or NaN are unspecified.
+ */
+dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activation, void* codes,
+                                void* sf, int32_t sf_packed, float* dbias, int64_t M, int64_t I,
+                                void* hip_stream);
 
 /*
  * Frees every library-owned buffer (split-K partials and counters, transposed operand
