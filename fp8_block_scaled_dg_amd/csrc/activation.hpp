@@ -37,9 +37,9 @@ __device__ __forceinline__ float act_bell(float z) {
   return __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
 }
 
-// t = 1 / (1 + 0.2687 z) and P(t), whose product is Phi(-z) e^(z^2/2), z = |x|
-__device__ __forceinline__ float act_tail_poly(float z, float& t) {
-  t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.26870056986808777f, z, 1.f));
+// t P(t) + add = Phi(-z) e^(z^2/2) + add, z = |x|; t P(t) alone to *plain, too
+__device__ __forceinline__ float act_tail(float z, float add, float* plain = nullptr) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.26870056986808777f, z, 1.f));
   float p = 0.02952457405626774f;
   p = __builtin_fmaf(p, t, -0.1313483715057373f);
   p = __builtin_fmaf(p, t, 0.1823785901069641f);
@@ -48,13 +48,8 @@ __device__ __forceinline__ float act_tail_poly(float z, float& t) {
   p = __builtin_fmaf(p, t, 0.06914930045604706f);
   p = __builtin_fmaf(p, t, 0.1020011231303215f);
   p = __builtin_fmaf(p, t, 0.1069524958729744f);
-  return __builtin_fmaf(p, t, 0.10720593482255936f);
-}
-
-// t P(t) + add
-__device__ __forceinline__ float act_tail(float z, float add) {
-  float t;
-  const float p = act_tail_poly(z, t);
+  p = __builtin_fmaf(p, t, 0.10720593482255936f);
+  if (plain) *plain = p * t;
   return __builtin_fmaf(p, t, add);
 }
 
@@ -136,9 +131,8 @@ __device__ __forceinline__ void gated_backward(const float (&d)[N], float (&g)[N
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float z = fabsf(g[i]), bell = act_bell(z);
-      float t;
-      const float p = act_tail_poly(z, t);
-      const float q = p * t * bell, s = __builtin_fmaf(p, t, -0.3989422804014327f * z) * bell;
+      float tail;
+      const float s = act_tail(z, -0.3989422804014327f * z, &tail) * bell, q = tail * bell;
       finish(i, g[i] * (g[i] > 0.f ? 1.f - q : q), g[i] > 0.f ? 1.f - s : s);
     }
   } else if (act == DG_ACT_GELU_TANH) {

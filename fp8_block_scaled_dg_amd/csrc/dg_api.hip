@@ -653,6 +653,10 @@ const CfgEntry kTable[] = {
      launch_ring<kRing128x128, kEpiBf16>, launch_ring<kRing128x128, kEpiFp8>},
     {"ring_n128_wide", nullptr, nullptr, nullptr, 64, kPipeMaxKB, nullptr,
      launch_ring<kRingStream, kEpiBf16>, launch_ring<kRingStream, kEpiFp8>},
+    // the gated product only, which chooses for itself (dg_block.hip); it also takes pipe128x256
+    {"gated_m16", nullptr, nullptr, nullptr, 0, kPipeMaxKB},
+    {"gated_m32", nullptr, nullptr, nullptr, 0, kPipeMaxKB},
+    {"gated_m64", nullptr, nullptr, nullptr, 0, kPipeMaxKB},
 };
 constexpr int kNumCfg = (int)(sizeof(kTable) / sizeof(kTable[0]));
 
@@ -789,6 +793,10 @@ dg_status launch(int kind, int id, const Problem& p, int64_t blocks, hipStream_t
 // ---------------------------------------------------------------- validation
 
 }  // namespace
+
+void print_dense_choice(int64_t M, int64_t N, int64_t K, const char* config, const char* note) {
+  maybe_print(kDense, M, N, K, 1, find_cfg(config), note);
+}
 
 dg_status check_common(const void* A, const void* B, const void* C, const void* sfA,
                        const float* sfB, int64_t N, int64_t K, bool any_output) {

@@ -4,10 +4,14 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
 
 #include "../../include/dg.h"
 #include "dropout.hpp"
 #include "gated_kernel.hpp"
+#include "gated_ring.hpp"
 #include "host.hpp"
 #include "layernorm_kernel.hpp"
 #include "pipe_kernel.hpp"
@@ -59,9 +63,116 @@ dg_status launch_pipe_gated(const Problem& p0, const Epilogue& ep, hipStream_t s
   return launched("pipe_kernel");
 }
 
+constexpr int64_t kLaunchThreads = (int64_t)1 << 32;  // a launch holds fewer
+
+template <class Cfg>
+dg_status launch_gated_ring_as(const Problem& p, int64_t S, const Epilogue& ep, hipStream_t stream) {
+  GatedArgs a{};
+  a.p = p;
+  a.ep = ep;
+  a.tiles_m = (int32_t)((p.M + Cfg::BM - 1) / Cfg::BM);
+  const int64_t tiles = a.tiles_m * (p.N / 256), pairs = (p.K / kKBlock + 1) / 2;
+  a.S = (int32_t)S;
+  a.KS = (int32_t)(2 * ((pairs + S - 1) / S));
+  const int64_t grid = tiles * S;
+  if (grid >= kLaunchThreads / Cfg::NT)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld workgroups", (long long)grid);
+  if (S > 1) {
+    const size_t part = (size_t)grid * 2 * Cfg::BM * 128 * sizeof(float);
+    const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
+    if (st != DG_OK) return st;
+  }
+  hipLaunchKernelGGL(gated_ring_kernel<Cfg>, dim3((unsigned)grid), dim3(Cfg::NT), 0, stream, a);
+  return launched("gated_ring_kernel");
+}
+
+template <bool PACKED, bool STREAM_B>
+dg_status launch_gated_ring(int bm, int64_t S, const Problem& p, const Epilogue& ep, hipStream_t st) {
+  if (bm == 16) return launch_gated_ring_as<GatedCfg<1, 1, 1, PACKED, STREAM_B>>(p, S, ep, st);
+  if (bm == 32) return launch_gated_ring_as<GatedCfg<2, 1, 2, PACKED, STREAM_B>>(p, S, ep, st);
+  return launch_gated_ring_as<GatedCfg<2, 2, 2, PACKED, STREAM_B>>(p, S, ep, st);
+}
+
+// Estimated times in us, fitted to measurements on one MI355X: 390 products of 1 to 2048 rows, 256
+// to 18432 columns of h, K = 512 to 18432, the kernels' every form that fits (bm rows, S splits),
+// most of them with so many weights in turn that each came from HBM. On them the choice is within
+// 1 % of the best form measured on average, within 10 % on all but a dozen (the worst, 1500 x 256 x
+// 2048: 15 - 29 %).
+//   ring: launch, prologue and epilogue; the run's pairs; B's bytes; further rounds of tiles; for
+//   S > 1 the partials' trip through memory and the last split's sum over them.
+//   us by S:            1     2     3     4     6     8    14
+//    M = 1,  I = 2048, K = 7168, bm = 16   37.8  23.3  18.9  15.5  14.0  13.2  14.4  (tiles 25.6)
+//    M = 64, I = 2048, K = 7168, bm = 64   47.1  30.0  25.2  21.6  20.0  19.9  24.1  (28.3)
+//    M = 64, I = 8192, K = 8192, bm = 64   56.8  41.5  33.1  32.4                    (54.1)
+//    M = 1000, I = 2048, K = 7168          46.5 (bm = 32: 76)                        (49.4)
+//    M = 2048, I = 2816, K = 4096          82.1                                      (68.9)
+struct GatedPlan {
+  int bm;  // 0: the tile kernel
+  int64_t S;
+  double time;
+};
+
+GatedPlan gated_ring_plan(int bm, int64_t M, int64_t I, int64_t K) {
+  const int k = bm == 16 ? 0 : bm == 32 ? 1 : 2;
+  const double start[] = {3.7, 4.1, 5.8}, pair[] = {0.93, 1.0, 1.2}, each[] = {0.24, 0.38, 0.78};
+  const int64_t pairs = (K / kKBlock + 1) / 2, tiles = (M + bm - 1) / bm * (I / 128);
+  const int64_t rounds = (tiles + kCUs - 1) / kCUs;
+  const double fixed = start[k] + (double)(2 * I) * (double)K / 11e6;
+  GatedPlan best{bm, 1, fixed + (double)rounds * pair[k] * (double)pairs + 4.2 * (double)(rounds - 1)};
+  for (int64_t S = 2; S <= 16 && S <= pairs && tiles * S <= kCUs; ++S) {
+    const int64_t run = (pairs + S - 1) / S, used = (pairs + run - 1) / run;
+    const double rows = M < bm ? (double)M / bm : 1.0;
+    const double t = fixed + pair[k] * (double)run + 2.0 + each[k] * rows * (double)used;
+    if (t < best.time) best = GatedPlan{bm, used, t};
+  }
+  return best;
+}
+
+double gated_pipe_time(int64_t M, int64_t I, int64_t K) {
+  const int64_t KB = K / kKBlock, tiles = (M + 127) / 128 * (I / 128);
+  const TailSplit ts = pipe_tail_split(tiles, KB);
+  const double round = 0.79 * (double)KB + 9.1, fixed = (double)(2 * I) * (double)K / 9.5e6 - 1.6;
+  if (ts.parts == 1) return fixed + (double)((tiles + kCUs - 1) / kCUs) * round;
+  return fixed + (double)(ts.full / kCUs) * round + 0.79 * (double)(KB / ts.parts) + 12.6 + 1.2 * (double)ts.parts;
+}
+
+// The tile kernel's 32-bit offsets reach from a gate row to its up row.
+bool gated_pipe_fits(int64_t I, int64_t K) { return (I + 256) * K < (int64_t)1 << 31; }
+
+GatedPlan gated_plan(int64_t M, int64_t I, int64_t K) {
+  const char* forced = getenv("DG_FORCE_CONFIG");
+  if (forced && strcmp(forced, "pipe128x256") == 0 && gated_pipe_fits(I, K)) return GatedPlan{0, 1, 0};
+  GatedPlan best{0, 1, gated_pipe_fits(I, K) ? gated_pipe_time(M, I, K) : 1e30};
+  for (int bm : {16, 32, 64}) {
+    const GatedPlan pl = gated_ring_plan(bm, M, I, K);
+    char name[16];
+    snprintf(name, sizeof name, "gated_m%d", bm);
+    if (forced && strcmp(forced, name) == 0) return pl;
+    if ((M + bm - 1) / bm * (I / 128) < kLaunchThreads / 512 && pl.time < best.time) best = pl;
+  }
+  return best;
+}
+
+// From this many bytes on B is streamed past the caches where one row tile reads it: by the ring
+// kernel's rule and for its reason. us, streamed and not, with so many weights in turn that none
+// stays in a cache: 64 x 18432 x 7168 56.8, 61.8; 1 x 18432 x 7168 48.1, 52.5; with a weight of
+// 75 MB that stays (1 x 2048 x 18432) 23.7, 18.6.
+constexpr int64_t kGatedStreamB = int64_t(96) << 20;
+
 dg_status gated(const Problem& p, const Epilogue& ep, hipStream_t stream) {
-  return p.K / kKBlock >= kLongKB ? launch_pipe_gated<PipeCfg<128, 256, 12>>(p, ep, stream)
-                                  : launch_pipe_gated<PipeCfg<128, 256>>(p, ep, stream);
+  const int64_t I = p.N / 2;
+  const GatedPlan pl = gated_plan(p.M, I, p.K);
+  if (pl.bm == 0) {
+    print_dense_choice(p.M, p.N, p.K, "pipe128x256", " (gated)");
+    return p.K / kKBlock >= kLongKB ? launch_pipe_gated<PipeCfg<128, 256, 12>>(p, ep, stream)
+                                    : launch_pipe_gated<PipeCfg<128, 256>>(p, ep, stream);
+  }
+  print_dense_choice(p.M, p.N, p.K, pl.bm == 16 ? "gated_m16" : pl.bm == 32 ? "gated_m32" : "gated_m64", " (gated)");
+  if (p.M <= pl.bm && p.N * p.K >= kGatedStreamB)
+    return p.sfa_packed ? launch_gated_ring<true, true>(pl.bm, pl.S, p, ep, stream)
+                        : launch_gated_ring<false, true>(pl.bm, pl.S, p, ep, stream);
+  return p.sfa_packed ? launch_gated_ring<true, false>(pl.bm, pl.S, p, ep, stream)
+                      : launch_gated_ring<false, false>(pl.bm, pl.S, p, ep, stream);
 }
 
 }  // namespace
@@ -224,8 +335,8 @@ dg_status dg_fp8_gemm_nt_gated_fp8(const void* A, const void* B, void* codes, vo
   if (!aligned(sf, 4)) return fail(DG_ERR_MISALIGNED, "sf must be 4-byte aligned");
   if (!aligned(bias, 16) || !aligned(pre, 16))
     return fail(DG_ERR_MISALIGNED, "bias and pre must be 16-byte aligned");
-  if (K / kKBlock > kPipeMaxKB || (I + 256) * K >= (int64_t)1 << 31)
-    return fail(DG_ERR_UNSUPPORTED_SHAPE, "K beyond 2^22, or (I + 256) * K beyond 2^31");
+  if (K / kKBlock > kPipeMaxKB || I / 128 * (K / kKBlock) >= (int64_t)1 << 28)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "K beyond 2^22, or I * K beyond 2^42");
   Problem p{};
   p.A = (const uint8_t*)A;
   p.B = (const uint8_t*)B;

@@ -23,6 +23,7 @@ dg_status get_workspace(hipStream_t stream, size_t partial_bytes, size_t counter
 dg_status check_common(const void* A, const void* B, const void* C, const void* sfA,
                        const float* sfB, int64_t N, int64_t K, bool any_output);
 dg_status check_rows(int64_t M, int64_t K, const char* k);
+void print_dense_choice(int64_t M, int64_t N, int64_t K, const char* config, const char* note);
 dg_status check_norm(int32_t x_dtype, int32_t w_dtype, int64_t M, int64_t K);
 dg_status launched(const char* what);
 dg_status get_partials(hipStream_t st, int64_t count, float** part);

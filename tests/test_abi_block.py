@@ -121,7 +121,7 @@ def test_gated_refuses(dg):
     for name in ("sf", "sA", "sB"):
         assert gated(dg, **{name: FAKE + 2}) == ALIGN, name
     assert gated(dg, M=(1 << 30) + 1) == BIG and gated(dg, I=(1 << 29) + 128) == BIG
-    assert gated(dg, K=(1 << 22) + 128) == BIG and gated(dg, I=1 << 20, K=1 << 11) == BIG
+    assert gated(dg, K=(1 << 22) + 128) == BIG and gated(dg, I=1 << 21, K=1 << 21) == BIG
     assert gated(dg, M=0) == "DG_OK" and gated(dg, I=0) == "DG_OK"
 
 

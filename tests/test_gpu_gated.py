@@ -60,6 +60,17 @@ def test_gated_integers(M, I, K):
         blk.check_fp8(h, dh, codes, sf, f"{act} {M}x{I}x{K}")
 
 
+@pytest.mark.parametrize("config", ["gated_m16", "gated_m32", "gated_m64", "pipe128x256"])
+@pytest.mark.parametrize("M,I,K", [(1, 256, 128), (20, 384, 640), (64, 2048, 7168), (130, 512, 896), (33, 128, 7296),
+                                   (300, 1152, 1920), (64, 7168, 7040)])
+def test_gated_configurations(M, I, K, config, monkeypatch):
+    # every kernel form, also where it would not be chosen: odd and even K-blocks, with and without
+    # K splits, rows in several tiles, B streamed past the caches
+    monkeypatch.setenv("DG_FORCE_CONFIG", config)
+    assert config in dg().config_names()
+    test_gated_integers(M, I, K)
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu_tanh"])
 @pytest.mark.parametrize("M,I,K", [(5, 256, 896), (64, 2048, 2048), (257, 384, 640)])
 def test_gated_other_activations(M, I, K, act):
