@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 
 #include "../../include/dg.h"
 #include "dropout.hpp"
@@ -30,6 +31,50 @@ dg_status drop_args(double p, const int64_t* rng, int64_t subsequence, DropArgs*
   if (!aligned(rng, 8)) return fail(DG_ERR_MISALIGNED, "rng must be 8-byte aligned");
   *d = DropArgs{threshold ? (const uint64_t*)rng : nullptr, (uint64_t)subsequence, threshold,
                 (float)(65536.0 / (65536.0 - threshold))};
+  return DG_OK;
+}
+
+// ---------------------------------------------------------------- column sums in one launch
+//
+// Up to these sizes the backward kernels sum columns in the same launch, in extra workgroups that
+// read the inputs a second time. Us, one launch against two, back to back calls (3 us of host time
+// for each launch) and in a graph:
+//   layer norm bf16   64 x 7168   7.3,  9.8    4.7,  8.5     512 x 7168  10.9, 17.6  11.1, 17.7
+//                    256 x 7168   7.5, 15.7    7.2, 15.8    1000 x 1024   7.3, 10.1   6.5,  7.9
+//                   1000 x 2048   9.0, 10.1    9.2,  9.7    1000 x 4096  15.4, 14.0  15.7, 14.2
+//              fp32  257 x 2048   7.5, 10.1    3.9,  7.4    2000 x 1024  11.1, 10.6  11.3, 10.2
+//                                                          512 x 16384              41.2, 38.2
+//   gated (gelu)     130 x 2048   6.6,  9.5    5.2,  7.1     257 x 2048   6.8,  9.5   6.8,  7.3
+//                    256 x 7168  10.1, 10.1   10.1,  9.9     512 x  512   8.4,  9.3   8.5,  7.0
+//   dropout fp32     512 x 7168   6.8,  9.3    6.8,  8.3    1000 x 2048   7.6,  9.4   7.6,  6.9
+//                   1000 x 4096   8.7,  9.3    8.8,  8.3    1000 x 7168  14.7, 11.3  14.9, 11.5
+// The bounds follow the calls: in a graph they give away up to 1 us near them. (The layer norm's
+// two launches move 4 K bytes of partials for each workgroup, 256 from 256 rows on.)
+constexpr int64_t kGatedDirectRows = 384, kDropDirectRows = 1024, kDropDirectValues = 1 << 22;
+bool ln_direct(int64_t M, int64_t K) {
+  return (M <= 512 && M * K <= 3 << 21) || (M <= 1024 && K <= 2048);
+}
+
+// R teams of a row's threads; LDS for their sums, or for the sums of workgroups that only sum.
+template <bool BF16, bool WBF, int C>
+dg_status launch_layernorm_backward(const LayerNormBwdArgs& a, unsigned grid, unsigned threads,
+                                    hipStream_t st) {
+  const auto kernel = layernorm_backward_kernel<BF16, WBF, C>;
+  constexpr bool lds_dw = kLnLdsDw<BF16, C>;
+  if (lds_dw) {  // up to 128 KB
+    static std::once_flag once;
+    static hipError_t attr_err = hipSuccess;
+    std::call_once(once, [&] {
+      attr_err = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     kNormMaxK * (int)sizeof(float));
+    });
+    if (attr_err != hipSuccess)
+      return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(attr_err));
+  }
+  size_t bytes = (size_t)(lds_dw ? a.K : (a.teams - 1) * a.K) * sizeof(float);
+  const size_t direct = (size_t)threads * 2 * Pieces<BF16>::P * sizeof(float);
+  if (!a.part && direct > bytes) bytes = direct;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), bytes, st, a);
   return DG_OK;
 }
 
@@ -225,7 +270,7 @@ dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropo
   const hipStream_t st = (hipStream_t)stream;
   if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, K, st) : DG_OK;
   const StripPlan pl = strip_plan(M, K);
-  const bool direct = dbias && M <= kDirectRows && M * K <= kDirectActValues, sum = dbias && !direct;
+  const bool direct = dbias && M <= kDropDirectRows && M * K <= kDropDirectValues, sum = dbias && !direct;
   float* part = nullptr;
   if (sum) {
     s = get_partials(st, pl.groups * K, &part);
@@ -233,7 +278,7 @@ dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropo
   }
   const DropBwdArgs a{dy, (uint8_t*)codes, ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(K / 128)}, part,
                       dbias, M, pl.rows, (int32_t)K, (int32_t)pl.strips, (int32_t)pl.groups, drop};
-  const dim3 grid((unsigned)(pl.strips * pl.groups + (direct ? K / 64 : 0)));
+  const dim3 grid((unsigned)(pl.strips * pl.groups + (direct ? K / kDropDirectCols : 0)));
   if (dy_dtype == DG_DTYPE_BF16)
     hipLaunchKernelGGL(dropout_backward_kernel<true>, grid, dim3(256), 0, st, a);
   else
@@ -265,12 +310,11 @@ dg_status dg_layernorm_fp8_1x128(const void* x, const void* residual, int32_t x_
   const int resident = norm_chunks(K) == 1 ? 1024 / nt : 1;  // as for the RMS norm
   const dim3 grid((unsigned)even_grid(M, kCUs * resident)), block((unsigned)nt);
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    constexpr bool ahead = c.value <= (xb.value ? 2 : 1);
     if (a.drop.threshold)
-      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, ahead, true>), grid, block, 0,
+      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, true>), grid, block, 0,
                          (hipStream_t)stream, a);
     else
-      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, ahead, false>), grid, block, 0,
+      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, false>), grid, block, 0,
                          (hipStream_t)stream, a);
   });
   return launched("layernorm_kernel");
@@ -298,7 +342,7 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
   if (R > (M + kCUs - 1) / kCUs) R = (M + kCUs - 1) / kCUs;
   const int64_t G = even_grid((M + R - 1) / R, kCUs);
   // a dx in the place of dy or h would be written while the column sums read them
-  const bool direct = M <= kDirectRows && dx != dy && dx != h;
+  const bool direct = ln_direct(M, K) && dx != dy && dx != h;
   float* part = nullptr;
   if (!direct) {
     s = get_partials(st, G * 2 * K, &part);
@@ -306,12 +350,13 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
   }
   const LayerNormBwdArgs a{dy, dh, h, weight, mean, rstd, dx, part, dweight, dbias, M, (int32_t)K,
                            (int32_t)R, (int32_t)G};
-  const unsigned grid = (unsigned)(G + (direct ? K / 64 : 0));
+  const unsigned grid = (unsigned)(G + (direct ? K / kLnDirectCols : 0));
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    constexpr bool ahead = c.value <= (xb.value ? 2 : 1);
-    hipLaunchKernelGGL((layernorm_backward_kernel<xb.value, wb.value, c.value, ahead>), dim3(grid),
-                       dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
+    s = no_throw([&] {
+      return launch_layernorm_backward<xb.value, wb.value, c.value>(a, grid, (unsigned)(nt * R), st);
+    });
   });
+  if (s != DG_OK) return s;
   s = launched("layernorm_backward_kernel");
   return s == DG_OK && !direct ? launch_column_sum2(part, dweight, dbias, G, K, st) : s;
 }
@@ -372,7 +417,7 @@ dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activat
   const hipStream_t st = (hipStream_t)stream;
   if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, 2 * I, st) : DG_OK;
   const StripPlan pl = strip_plan(M, I);
-  const bool direct = dbias && M <= kDirectRows && M * I <= kDirectActValues, sum = dbias && !direct;
+  const bool direct = dbias && M <= kGatedDirectRows && M * I <= kDirectActValues, sum = dbias && !direct;
   float* part = nullptr;
   if (sum) {
     s = get_partials(st, pl.groups * 2 * I, &part);
@@ -381,7 +426,7 @@ dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activat
   const GatedBwdArgs a{(const uint16_t*)dh, (const uint16_t*)pre, (uint8_t*)codes,
                        ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(I / 64)}, part, dbias, M, pl.rows,
                        (int32_t)I, activation, (int32_t)pl.strips, (int32_t)pl.groups};
-  hipLaunchKernelGGL(gated_backward_kernel, dim3((unsigned)(pl.strips * pl.groups + (direct ? I / 64 : 0))),
+  hipLaunchKernelGGL(gated_backward_kernel, dim3((unsigned)(pl.strips * pl.groups + (direct ? I / kGatedDirectCols : 0))),
                      dim3(256), 0, st, a);
   s = launched("gated_backward_kernel");
   return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, 2 * I, st) : s;

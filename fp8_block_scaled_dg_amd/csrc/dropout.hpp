@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_add_kernel(DropAddArgs a
 
 // ---------------------------------------------------------------- its gradient, FP8 output
 
+constexpr int kDropDirectCols = 32;  // columns of a workgroup that only sums
+
 struct DropBwdArgs {
   const void* dy;
   uint8_t* codes;
@@ -257,14 +259,15 @@ __global__ void __launch_bounds__(256) dropout_backward_kernel(DropBwdArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int)blockIdx.x >= a.strips * a.groups) {
     constexpr int P = Pieces<BF16>::P;
-    direct_column_sums<P, 256>(a.M, ((int)blockIdx.x - a.strips * a.groups) * 64, a.dbias,
-                               [&](int64_t m, int c, float (&v)[P]) {
-                                 float d[P];
-                                 load_piece<BF16>(a.dy, m * a.K + c, d);
-                                 drop_piece<BF16>(drop, m * a.K + c, d);
+    direct_sums<1, P, kDropDirectCols>(
+        a.M, ((int)blockIdx.x - a.strips * a.groups) * kDropDirectCols, {a.dbias}, &sums[0][0],
+        [&](int64_t m, int c, float (&v)[1][P]) {
+          float d[P];
+          load_piece<BF16>(a.dy, m * a.K + c, d);
+          drop_piece<BF16>(drop, m * a.K + c, d);
 #pragma unroll
-                                 for (int i = 0; i < P; ++i) v[i] += d[i];
-                               });
+          for (int i = 0; i < P; ++i) v[0][i] += d[i];
+        });
     return;
   }
   const int strip = blockIdx.x % a.strips, group = blockIdx.x / a.strips;

@@ -11,6 +11,8 @@
 
 namespace dg {
 
+constexpr int kGatedDirectCols = 32;  // columns of a workgroup that only sums
+
 struct GatedBwdArgs {
   const uint16_t* dh;
   const uint16_t* pre;
@@ -33,17 +35,17 @@ static __global__ void __launch_bounds__(256) gated_backward_kernel(GatedBwdArgs
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t I = a.I, N = 2 * I;
   if ((int)blockIdx.x >= a.strips * a.groups) {
-    const int col0 = ((int)blockIdx.x - a.strips * a.groups) * 64;
-    direct_column_sums2<8, 256>(a.M, col0, a.dbias, a.dbias + I,
-                                [&](int64_t m, int c, float (&v)[8], float (&u)[8]) {
-                                  float d[8], g[8], x[8];
-                                  load_piece<true>(a.dh, m * I + c, d);
-                                  load_piece<true>(a.pre, m * N + c, g);
-                                  load_piece<true>(a.pre, m * N + I + c, x);
-                                  gated_backward(d, g, x, a.act);
+    direct_sums<2, 8, kGatedDirectCols>(
+        a.M, ((int)blockIdx.x - a.strips * a.groups) * kGatedDirectCols, {a.dbias, a.dbias + I}, &sums[0][0][0],
+        [&](int64_t m, int c, float (&v)[2][8]) {
+          float d[8], g[8], x[8];
+          load_piece<true>(a.dh, m * I + c, d);
+          load_piece<true>(a.pre, m * N + c, g);
+          load_piece<true>(a.pre, m * N + I + c, x);
+          gated_backward(d, g, x, a.act);
 #pragma unroll
-                                  for (int i = 0; i < 8; ++i) v[i] += g[i], u[i] += x[i];
-                                });
+          for (int i = 0; i < 8; ++i) v[0][i] += g[i], v[1][i] += x[i];
+        });
     return;
   }
   const int strip = blockIdx.x % a.strips, group = blockIdx.x / a.strips;

@@ -24,11 +24,14 @@
 
 namespace dg {
 
-// Sum of v over the wave's 64 lanes, in each of them.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum of v over groups of 8 lanes and over the wave's 64, in each of them.
+__device__ __forceinline__ float sum8(float v) {
   v += dppf<kDppXor1>(v);
   v += dppf<kDppXor2>(v);
-  v += dppf<kDppMirror8>(v);
+  return v + dppf<kDppMirror8>(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum8(v);
   v += dppf<kDppMirror16>(v);
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
@@ -50,29 +53,36 @@ struct LayerNormArgs {
   DropArgs drop;
 };
 
-// The rows and chunks of rmsnorm_kernel. AHEAD: weights and bias stay in registers and the
-// next row is loaded before the barrier of this one.
-template <bool BF16, bool WBF, int C, bool AHEAD, bool DROP>
+// The rows and chunks of rmsnorm_kernel. KEEP: weights and bias stay in registers; otherwise
+// (long rows) they are loaded where they are used. AHEAD: the next row is loaded before the
+// barrier of this one, which only the longest fp32 rows leave no registers for.
+template <bool BF16, bool WBF, int C, bool DROP>
 __global__ void __launch_bounds__(kNormThreads) layernorm_kernel(LayerNormArgs a) {
-  __shared__ float buf[2][2][kNormThreads / 64];
-  __shared__ float counts[kNormThreads / 64];
+  constexpr bool KEEP = C <= (BF16 ? 2 : 1), AHEAD = BF16 || C <= 3;
+  static_assert(kNormThreads / 64 == 8, "a row's waves fit 8 lanes");
+  __shared__ float buf[2][2][8];  // means and squares of the waves; two in turn
   const int K = a.K, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const float inv_k = 1.f / (float)K;
   const Drop drop(a.drop);
   int col[C];
-  Weight16<BF16, WBF> w[C], b[C];
+  Weight16<BF16, WBF> w[KEEP ? C : 1], b[KEEP ? C : 1];
   Raw16<BF16> x[C], r[C];
-  int live = 0;  // the wave's lanes with values, over its chunks
+  // values that the wave in question holds: this one, and wave i in lanes i, i + 8, ...
+  auto count_of = [&](int v) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) n += max(0, min(1024, K - 16 * (int)(c * blockDim.x + 64 * v)));
+    return (float)n;
+  };
+  const float count = count_of(wave), peer = (int)(threadIdx.x & 7) < waves ? count_of(threadIdx.x & 7) : 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     col[c] = norm_col<BF16>(c, blockDim.x, threadIdx.x);
-    live += __popcll(__ballot(col[c] < K));
-    if (AHEAD && col[c] < K) {
+    if (KEEP && col[c] < K) {
       w[c].load(a.w, col[c]);
       if (a.b) b[c].load(a.b, col[c]);
     }
   }
-  const float count = 16.f * (float)live;  // > 0: a row's threads end with a wave that has some
-  if ((threadIdx.x & 63) == 0) counts[wave] = count;
   auto fetch = [&](int64_t m) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -101,8 +111,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_kernel(LayerNormArgs a
       for (int i = 0; i < 16; ++i) sum += v[c][i];
     }
     if (AHEAD && m + gridDim.x < a.M) fetch(m + gridDim.x);
-    sum = wave_sum(sum);
-    const float own = sum / count;
+    const float own = wave_sum(sum) / count;
     float sq = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -116,14 +125,11 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_kernel(LayerNormArgs a
     sq = wave_sum(sq);
     if ((threadIdx.x & 63) == 0) buf[par][0][wave] = own, buf[par][1][wave] = sq;
     lds_barrier();
-    float mean = 0.f, var = 0.f;
-    for (int i = 0; i < waves; ++i) mean = __builtin_fmaf(counts[i], buf[par][0][i], mean);
-    mean /= (float)K;
-    for (int i = 0; i < waves; ++i) {
-      const float d = buf[par][0][i] - mean;
-      var += __builtin_fmaf(counts[i] * d, d, buf[par][1][i]);
-    }
-    const float rstd = 1.f / sqrtf(var / (float)K + a.eps);
+    const float theirs = peer > 0.f ? buf[par][0][threadIdx.x & 7] : 0.f;
+    const float squares = peer > 0.f ? buf[par][1][threadIdx.x & 7] : 0.f;
+    const float mean = sum8(peer * theirs) * inv_k;
+    const float var = sum8(__builtin_fmaf(peer * (theirs - mean), theirs - mean, squares)) * inv_k;
+    const float rstd = 1.f / sqrtf(var + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[m] = mean;
       if (a.rstd) a.rstd[m] = rstd;
@@ -132,20 +138,23 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_kernel(LayerNormArgs a
     for (int c = 0; c < C; ++c) {
       if (col[c] >= K) continue;
       if (a.h) store16<BF16>(a.h, m * K + col[c], v[c]);
-      if (!AHEAD) {
-        w[c].load(a.w, col[c]);
-        if (a.b) b[c].load(a.b, col[c]);
+      const int k = KEEP ? c : 0;
+      if (!KEEP) {
+        w[0].load(a.w, col[c]);
+        if (a.b) b[0].load(a.b, col[c]);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[c][i] = (v[c][i] - mean) * rstd * w[c][i];
+      for (int i = 0; i < 16; ++i) v[c][i] = (v[c][i] - mean) * rstd * w[k][i];
       if (a.b) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[c][i] += b[c][i];
+        for (int i = 0; i < 16; ++i) v[c][i] += b[k][i];
       }
       quantize16<BF16>(v[c], threadIdx.x & 7, m, col[c] >> 7, a.codes, a.so);
     }
   }
 }
+
+constexpr int kLnDirectCols = 32;  // columns of a workgroup that only sums
 
 struct LayerNormBwdArgs {
   const void* dy;
@@ -164,42 +173,64 @@ struct LayerNormBwdArgs {
   int32_t groups;  // workgroups that take rows
 };
 
+// Values added to a lane's 16 fp32 sums in LDS (its own, so nothing has to be waited for).
+template <bool BF16>
+__device__ __forceinline__ void lds_add16(float* sums, const float (&v)[16]) {
+  constexpr int P = Pieces<BF16>::P;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    nk_v4f* p = (nk_v4f*)(sums + i / P * 8 * P + i % P);
+    const nk_v4f t = *p;
+    *p = nk_v4f{t[0] + v[i], t[1] + v[i + 1], t[2] + v[i + 2], t[3] + v[i + 3]};
+  }
+}
+
 // The teams and chunks of rmsnorm_backward_kernel, with two sums per row and two per column.
-template <bool BF16, bool WBF, int C, bool AHEAD>
+// LDS_DW: the sums of dweight lie in LDS, those of dbias in registers, which do not hold both
+// beside the values of a row in several chunks (registers alone spill 77 to 169 of them from
+// 16384 fp32 values on, 1000 x 18432: 121 us). AHEAD as there.
+template <bool BF16, int C>
+constexpr bool kLnLdsDw = C >= (BF16 ? 3 : 2);
+
+template <bool BF16, bool WBF, int C>
 __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerNormBwdArgs a) {
+  constexpr bool LDS_DW = kLnLdsDw<BF16, C>, AHEAD = C <= 2;
   __shared__ float buf[2][2][kNormThreads / 64];
-  extern __shared__ float teams_sums[];  // [teams - 1][K]
+  extern __shared__ float lds[];  // [teams - 1][K], LDS_DW: [K]; or the direct sums'
   const int K = a.K, R = a.teams, threads = blockDim.x / R;
+  const float inv_k = 1.f / (float)K;
   if ((int)blockIdx.x >= a.groups) {
     constexpr int P = Pieces<BF16>::P;
-    direct_column_sums2<P, kNormThreads>(
-        a.M, ((int)blockIdx.x - a.groups) * 64, a.dweight, a.dbias,
-        [&](int64_t m, int c, float (&v)[P], float (&u)[P]) {
+    direct_sums<2, P, kLnDirectCols>(
+        a.M, ((int)blockIdx.x - a.groups) * kLnDirectCols, {a.dweight, a.dbias}, lds,
+        [&](int64_t m, int c, float (&v)[2][P]) {
           float d[P], x[P];
           load_piece<BF16>(a.dy, m * K + c, d);
           load_piece<BF16>(a.h, m * K + c, x);
           const float mean = a.mean[m], rstd = a.rstd[m];
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            v[i] = __builtin_fmaf(d[i], (x[i] - mean) * rstd, v[i]);
-            u[i] += d[i];
+            v[0][i] = __builtin_fmaf(d[i], (x[i] - mean) * rstd, v[0][i]);
+            v[1][i] += d[i];
           }
         });
     return;
   }
   const int team = threadIdx.x / threads, t = threadIdx.x - team * threads;
   const int wave = t >> 6, waves = threads >> 6;
+  const bool peer = (int)(threadIdx.x & 7) < waves;
   int col[C];
-  Weight16<BF16, WBF> w[C];
-  float dw[C][16], db[C][16];
+  Weight16<BF16, WBF> w[AHEAD ? C : 1];
+  float dw[LDS_DW ? 1 : C][16], db[C][16];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     col[c] = norm_col<BF16>(c, threads, t);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[c][i] = db[c][i] = 0.f;
+    for (int i = 0; i < 16; ++i) dw[LDS_DW ? 0 : c][i] = db[c][i] = 0.f;
+    if (LDS_DW && col[c] < K) store_sums16<BF16>(lds + col[c], dw[0]);
     if (AHEAD && col[c] < K) w[c].load(a.w, col[c]);
   }
-  Raw16<BF16> h[C], dy[C], dh[C];
+  Raw16<BF16> h[C], dy[C], dh[AHEAD ? C : 1];
   float mu = 0.f, rs = 0.f;
   auto fetch = [&](int64_t m) {
     mu = a.mean[m];
@@ -214,7 +245,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
   auto fetch_dh = [&](int64_t m) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (col[c] < K && a.dh) dh[c].load(a.dh, m * K + col[c]);
+      if (AHEAD && col[c] < K && a.dh) dh[c].load(a.dh, m * K + col[c]);
   };
   const int64_t step = (int64_t)a.groups * R;
   int64_t m = (int64_t)blockIdx.x * R + team;
@@ -233,18 +264,21 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (col[c] >= K) continue;
-        if (!AHEAD) w[c].load(a.w, col[c]);
         const int k = AHEAD ? c : 0;
+        if (!AHEAD) w[0].load(a.w, col[c]);
+        float p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float d = dy[c][i];
           xh[k][i] = (h[c][i] - mean) * rstd;
-          dw[c][i] = __builtin_fmaf(d, xh[k][i], dw[c][i]);
+          if (LDS_DW) p[i] = d * xh[k][i];
+          else dw[LDS_DW ? 0 : c][i] = __builtin_fmaf(d, xh[k][i], dw[LDS_DW ? 0 : c][i]);
           db[c][i] += d;
-          g[k][i] = d * w[c][i];
+          g[k][i] = d * w[k][i];
           sum += g[k][i];
           dot = __builtin_fmaf(g[k][i], xh[k][i], dot);
         }
+        if (LDS_DW && a.part) lds_add16<BF16>(lds + col[c], p);
       }
     }
     if (AHEAD && m + step < a.M) fetch(m + step);
@@ -255,25 +289,23 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
       buf[par][1][team * waves + wave] = dot;
     }
     lds_barrier();
-    sum = dot = 0.f;
-    for (int i = 0; i < waves; ++i) sum += buf[par][0][team * waves + i], dot += buf[par][1][team * waves + i];
-    sum /= (float)K;
-    dot /= (float)K;
+    sum = sum8(peer ? buf[par][0][team * waves + (threadIdx.x & 7)] : 0.f) * inv_k;
+    dot = sum8(peer ? buf[par][1][team * waves + (threadIdx.x & 7)] : 0.f) * inv_k;
     if (live) {
-      if (!AHEAD) fetch_dh(m);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         if (col[c] >= K) continue;
         const int k = AHEAD ? c : 0;
         if (!AHEAD) {
-          w[c].load(a.w, col[c]);
+          if (a.dh) dh[0].load(a.dh, m * K + col[c]);
+          w[0].load(a.w, col[c]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) xh[k][i] = (h[c][i] - mean) * rstd, g[k][i] = dy[c][i] * w[c][i];
+          for (int i = 0; i < 16; ++i) xh[0][i] = (h[c][i] - mean) * rstd, g[0][i] = dy[c][i] * w[0][i];
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           g[k][i] = rstd * __builtin_fmaf(-xh[k][i], dot, g[k][i] - sum);
-          if (a.dh) g[k][i] += dh[c][i];
+          if (a.dh) g[k][i] += dh[k][i];
         }
         store16<BF16>(a.dx, m * K + col[c], g[k]);
       }
@@ -281,28 +313,39 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
     if (AHEAD && m + step < a.M) fetch_dh(m + step);
   }
   if (!a.part) return;
-  // one sum after the other through the same LDS; every team passes every barrier
-#pragma unroll
-  for (int k = 0; k < 2 && R > 1; ++k) {
-    float(&own)[C][16] = k ? db : dw;
-    if (k) __syncthreads();
+  float* part = a.part + (int64_t)blockIdx.x * 2 * K;
+  if constexpr (LDS_DW) {  // R = 1
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (team > 0 && col[c] < K) store_sums16<BF16>(teams_sums + (team - 1) * K + col[c], own[c]);
-    __syncthreads();
-    for (int q = 0; q < R - 1 && team == 0; ++q)
+      if (col[c] < K) {
+        float v[16] = {};
+        add_sums16<BF16>(lds + col[c], v);
+        store_sums16<BF16>(part + col[c], v);
+        store_sums16<BF16>(part + K + col[c], db[c]);
+      }
+  } else {
+    // one sum after the other through the same LDS; every team passes every barrier
+#pragma unroll
+    for (int k = 0; k < 2 && R > 1; ++k) {
+      float(&own)[C][16] = k ? db : dw;
+      if (k) __syncthreads();
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (col[c] < K) add_sums16<BF16>(teams_sums + q * K + col[c], own[c]);
-  }
-  if (team > 0) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * K;
+        if (team > 0 && col[c] < K) store_sums16<BF16>(lds + (team - 1) * K + col[c], own[c]);
+      __syncthreads();
+      for (int q = 0; q < R - 1 && team == 0; ++q)
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    if (col[c] < K) {
-      store_sums16<BF16>(part + col[c], dw[c]);
-      store_sums16<BF16>(part + K + col[c], db[c]);
+        for (int c = 0; c < C; ++c)
+          if (col[c] < K) add_sums16<BF16>(lds + q * K + col[c], own[c]);
     }
+    if (team > 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col[c] < K) {
+        store_sums16<BF16>(part + col[c], dw[c]);
+        store_sums16<BF16>(part + K + col[c], db[c]);
+      }
+  }
 }
 
 }  // namespace dg

@@ -244,25 +244,38 @@ __device__ __forceinline__ void direct_column_sums(int64_t M, int col0, float* o
   }
 }
 
-// The same for two sums per column: add(m, col, v, u). out_u may be NULL: only v's are stored.
-template <int P, int NT, class F>
-__device__ __forceinline__ void direct_column_sums2(int64_t M, int col0, float* out_v, float* out_u,
-                                                    F add) {
-  constexpr int L = 64 / P;
-  __shared__ float sums[2][NT / L][64];
+// The same for NS sums of each of COLS columns, to out[0 .. NS - 1] (NULL: not stored), with four
+// rows' loads in flight: add(m, col, v) adds row m's values to v[0 .. NS - 1]. sums: LDS for
+// NS * P floats of every thread.
+template <int NS, int P, int COLS, class F>
+__device__ __forceinline__ void direct_sums(int64_t M, int col0, float* const (&out)[NS], float* sums,
+                                            F add) {
+  constexpr int L = COLS / P;  // lanes to a row
+  static_assert(COLS % P == 0 && 64 % L == 0, "whole rows per wave");
   const int groups = blockDim.x / L, r = threadIdx.x / L, c = (threadIdx.x % L) * P;
-  float v[P], u[P];
+  float v[NS][P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) v[i] = u[i] = 0.f;
-  for (int64_t m = r; m < M; m += groups) add(m, col0 + c, v, u);
+  for (int k = 0; k < NS; ++k)
 #pragma unroll
-  for (int i = 0; i < P; ++i) sums[0][r][c + i] = v[i], sums[1][r][c + i] = u[i];
-  __syncthreads();
-  for (int k = threadIdx.x; k < (out_u ? 128 : 64); k += blockDim.x) {
-    float s = 0.f;
-    for (int i = 0; i < groups; ++i) s += sums[k >> 6][i][k & 63];
-    (k < 64 ? out_v : out_u)[col0 + (k & 63)] = s;
+    for (int i = 0; i < P; ++i) v[k][i] = 0.f;
+  int64_t m = r;
+  for (; m + 3 * groups < M; m += 4 * groups) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) add(m + u * groups, col0 + c, v);
   }
+  for (; m < M; m += groups) add(m, col0 + c, v);
+#pragma unroll
+  for (int k = 0; k < NS; ++k)
+#pragma unroll
+    for (int i = 0; i < P; ++i) sums[(k * groups + r) * COLS + c + i] = v[k][i];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < NS; ++k)
+    for (int n = threadIdx.x; n < COLS && out[k]; n += blockDim.x) {
+      float s = 0.f;
+      for (int i = 0; i < groups; ++i) s += sums[(k * groups + i) * COLS + n];
+      out[k][col0 + n] = s;
+    }
 }
 
 // P consecutive values of a bf16 (P = 8) or fp32 (P = 4) array, 16 bytes.
