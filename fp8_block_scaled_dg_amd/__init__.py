@@ -1,6 +1,6 @@
 """Python binding of libdg.so, the MI355X (gfx950) FP8 block-scaled GEMM library.
 
-Argument marshalling only: every call checks dtypes, devices, shapes and contiguity,
+Argument marshalling only (in part native, csrc/marshal.cpp): every call checks dtypes, devices, shapes and contiguity,
 then passes raw device pointers and torch's current HIP stream to the C ABI declared
 in ``include/dg.h``. All arithmetic runs in the library's HIP kernels; there is no
 fallback path. If libdg.so is missing the import fails.
@@ -41,9 +41,12 @@ import torch  # loaded first: the library then binds to torch's HIP runtime
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdg.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(
-        f"{LIB_PATH} is not built; run `python fp8_block_scaled_dg_amd/build.py` (hipcc, gfx950)")
+for _path in (LIB_PATH, os.path.join(_PKG, "_marshal.so")):
+    if not os.path.exists(_path):
+        raise ImportError(
+            f"{_path} is not built; run `python fp8_block_scaled_dg_amd/build.py` (hipcc, gfx950)")
+
+from . import _marshal  # noqa: E402
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -62,9 +65,10 @@ def _check_current() -> None:
         want = _build.source_hash()
     except OSError:  # sources not shipped: nothing to compare with
         return
-    if want != BUILD_ID:
-        raise ImportError(f"{LIB_PATH} was built from other sources (build id {BUILD_ID}, "
-                          f"sources {want}); rebuild it: python fp8_block_scaled_dg_amd/build.py")
+    for path, got in ((LIB_PATH, BUILD_ID), (_marshal.__file__, _marshal.BUILD_ID)):
+        if want != got:
+            raise ImportError(f"{path} was built from other sources (build id {got}, "
+                              f"sources {want}); rebuild it: python fp8_block_scaled_dg_amd/build.py")
 
 
 _check_current()
@@ -133,6 +137,10 @@ lib.dg_dropout_add.argtypes = [_vp, _vp, _i32, ctypes.c_double, _vp, _i64, _vp, 
 lib.dg_dropout_backward_fp8.restype = ctypes.c_int
 lib.dg_dropout_backward_fp8.argtypes = [_vp, _i32, ctypes.c_double, _vp, _i64, _vp, _vp, _i32, _vp, _i64,
                                         _i64, _vp]
+
+_marshal.bind(*(ctypes.cast(f, _vp).value for f in (
+    lib.dg_layernorm_fp8_1x128, lib.dg_layernorm_backward, lib.dg_fp8_gemm_nt_gated_fp8,
+    lib.dg_gated_backward_fp8, lib.dg_dropout_add, lib.dg_dropout_backward_fp8)))
 
 lib.dg_release_workspaces.restype = ctypes.c_int
 lib.dg_release_workspaces.argtypes = []
@@ -576,6 +584,11 @@ def bias_act_backward_fp8(dc, pre=None, activation=None, codes=None, sf=None, db
     return codes, sf, dbias
 
 
+# The calls below first go through csrc/marshal.cpp, which returns None unless every argument is
+# as the call wants it and on the current GPU; the Python code behind it then raises the specific
+# error, or makes the call on another GPU. (layernorm_fp8_1x128 of one row takes the host 8.4 us
+# through Python's checks.)
+
 def _rng(rng, x: torch.Tensor, index: int):
     """rng's address: int64 [2] on x's GPU, (seed, offset); None without one."""
     return None if rng is None else _ptr(rng, "rng", torch.int64, (2,), x, index)
@@ -589,6 +602,10 @@ def layernorm_fp8_1x128(x, weight, bias=None, eps=1e-5, residual=None, h=None, m
     sum before the norm (it may be x or residual itself), mean and rstd (fp32 [M]) the row's
     statistics; layernorm_backward takes all three. dropout_p, rng and subsequence as in
     dropout_add."""
+    done = _marshal.layernorm(x, weight, bias, eps, residual, h, mean, rstd, codes, sf, ue8m0, dropout_p, rng,
+                              subsequence)
+    if done is not None:
+        return done
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     dtype, w_dtype = _float_type(x, "x"), _float_type(weight, "weight")
@@ -613,6 +630,9 @@ def layernorm_backward(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=None
     float32, None with need_dbias=False). dh, the gradient that reaches h along the residual
     stream, is added to dx; dx is the gradient of the sum before the norm (the residual's as it
     is, x's through dropout) and may be dy, dh or h itself."""
+    done = _marshal.layernorm_backward(dy, h, weight, mean, rstd, dh, dx, dweight, dbias, need_dbias)
+    if done is not None:
+        return done
     if h.dim() != 2:
         raise ValueError("h must be [M, K]")
     dtype, w_dtype = _float_type(h, "h"), _float_type(weight, "weight")
@@ -643,13 +663,17 @@ def fp8_gemm_nt_gated_fp8(a, b, a_sf, b_sf, bias=None, activation="silu", pre=No
     (codes [M, I] e4m3fn, sf), the down projection's a and a_sf (sf as in rmsnorm_fp8_1x128).
     I % 128 == 0; pre, when passed, receives z (bf16 [M, 2I], for gated_backward_fp8); the other
     arguments as for fp8_gemm_nt_bias_act_fp8."""
+    act = _act(activation)
+    done = _marshal.gated(a, b, a_sf, b_sf, bias, act, pre, codes, sf, ue8m0)
+    if done is not None:
+        return done
     M, N, K, dev, ap, bp, sa, packed, sb, bias_ptr, bias_dtype, pre_ptr = \
         _bias_act_operands(a, b, a_sf, b_sf, bias, pre)
     if N % 2:
         raise ValueError("b must be [2I, K]: gate rows, then up rows")
     codes, cp, sf, sp, sf_packed = _fp8_outputs(M, N // 2, codes, sf, ue8m0, a, dev)
     _launch(dev, lib.dg_fp8_gemm_nt_gated_fp8, ap, bp, cp, sp, sf_packed, sa, packed, sb, bias_ptr,
-            bias_dtype, _act(activation), pre_ptr, M, N // 2, K)
+            bias_dtype, act, pre_ptr, M, N // 2, K)
     return codes, sf
 
 
@@ -660,6 +684,10 @@ def gated_backward_fp8(dh, pre, activation="silu", codes=None, sf=None, dbias=No
     [M, 2I], sf, dbias): p quantized per 1x128 block and dbias [2I] float32 = p summed over rows
     (None with need_dbias=False). The input's gradient is then fp8_gemm_nn(codes, b, da, sf,
     b_sf.t().contiguous()) with the forward call's b."""
+    act = _act(activation)
+    done = _marshal.gated_backward(dh, pre, act, codes, sf, dbias, need_dbias, ue8m0)
+    if done is not None:
+        return done
     if dh.dim() != 2:
         raise ValueError("dh must be [M, I]")
     M, I = shape = dh.shape
@@ -670,7 +698,7 @@ def gated_backward_fp8(dh, pre, activation="silu", codes=None, sf=None, dbias=No
     if dbias is None and need_dbias:
         dbias = torch.empty((2 * I,), dtype=torch.float32, device=dh.device)
     db = None if dbias is None else _ptr(dbias, "dbias", torch.float32, (2 * I,), dh, dev)
-    _launch(dev, lib.dg_gated_backward_fp8, d, z, _act(activation), cp, sp, packed, db, M, I)
+    _launch(dev, lib.dg_gated_backward_fp8, d, z, act, cp, sp, packed, db, M, I)
     return codes, sf, dbias
 
 
@@ -682,6 +710,9 @@ def dropout_add(x, p, rng, subsequence=0, residual=None, out=None):
     loop counts the offset up, in a captured graph too, and gives each layer its subsequence. No
     mask is stored: backward calls name the same values. Returns out, which may be x or residual
     itself. Without a residual this is dropout's own gradient too."""
+    done = _marshal.dropout_add(x, p, rng, subsequence, residual, out)
+    if done is not None:
+        return done
     dtype = _float_type(x, "x")
     dev = _first(x, "x")
     r = None if residual is None else _ptr(residual, "residual", x.dtype, x.shape, x, dev)
@@ -698,6 +729,9 @@ def dropout_backward_fp8(dy, p, rng, subsequence=0, codes=None, sf=None, dbias=N
     projection before it: q = dropout(dy) for dy [M, K] (float32 or bfloat16) and the forward
     call's p, rng values and subsequence, returned as (codes [M, K], sf, dbias): q quantized per
     1x128 block and dbias [K] float32 = q summed over rows (None with need_dbias=False)."""
+    done = _marshal.dropout_backward(dy, p, rng, subsequence, codes, sf, dbias, need_dbias, ue8m0)
+    if done is not None:
+        return done
     if dy.dim() != 2:
         raise ValueError("dy must be [M, K]")
     dtype = _float_type(dy, "dy")
