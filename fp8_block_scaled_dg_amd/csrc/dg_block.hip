@@ -37,23 +37,21 @@ dg_status drop_args(double p, const int64_t* rng, int64_t subsequence, DropArgs*
 // ---------------------------------------------------------------- column sums in one launch
 //
 // Up to these sizes the backward kernels sum columns in the same launch, in extra workgroups that
-// read the inputs a second time. Us, one launch against two, back to back calls (3 us of host time
-// for each launch) and in a graph:
-//   layer norm bf16   64 x 7168   7.3,  9.8    4.7,  8.5     512 x 7168  10.9, 17.6  11.1, 17.7
-//                    256 x 7168   7.5, 15.7    7.2, 15.8    1000 x 1024   7.3, 10.1   6.5,  7.9
-//                   1000 x 2048   9.0, 10.1    9.2,  9.7    1000 x 4096  15.4, 14.0  15.7, 14.2
-//              fp32  257 x 2048   7.5, 10.1    3.9,  7.4    2000 x 1024  11.1, 10.6  11.3, 10.2
-//                                                          512 x 16384              41.2, 38.2
-//   gated (gelu)     130 x 2048   6.6,  9.5    5.2,  7.1     257 x 2048   6.8,  9.5   6.8,  7.3
-//                    256 x 7168  10.1, 10.1   10.1,  9.9     512 x  512   8.4,  9.3   8.5,  7.0
-//   dropout fp32     512 x 7168   6.8,  9.3    6.8,  8.3    1000 x 2048   7.6,  9.4   7.6,  6.9
-//                   1000 x 4096   8.7,  9.3    8.8,  8.3    1000 x 7168  14.7, 11.3  14.9, 11.5
-// The bounds follow the calls: in a graph they give away up to 1 us near them. (The layer norm's
-// two launches move 4 K bytes of partials for each workgroup, 256 from 256 rows on.)
-constexpr int64_t kGatedDirectRows = 384, kDropDirectRows = 1024, kDropDirectValues = 1 << 22;
-bool ln_direct(int64_t M, int64_t K) {
-  return (M <= 512 && M * K <= 3 << 21) || (M <= 1024 && K <= 2048);
-}
+// read the inputs a second time. Us in a graph, so many buffers in turn that they come from HBM, one
+// launch against two:
+//             layer norm bf16         gated (gelu)            dropout fp32
+//    130 x 2048   4.9,  7.0             6.9,  7.5               3.3, 6.0
+//    256 x 2048   5.6,  8.2             8.4,  8.0               4.3, 6.3
+//    512 x 2048   8.3,  9.4            13.9,  9.2               6.3, 6.8
+//    700 x 2048  12.4,  9.9            17.8, 10.8               8.2, 7.6
+//    130 x 7168   7.9, 11.6             8.3,  9.2               4.8, 6.7
+//    256 x 7168   9.8, 16.0            12.3, 11.5               5.8, 8.3
+//    512 x 7168  14.4, 17.7            19.9, 14.8               9.0, 10.0
+//    700 x 7168  17.3, 19.0            26.7, 19.3              12.9, 11.9
+// and the layer norm's gradient of 512 x 16384 fp32 41.2, 38.2. (Its two launches move 4 K bytes of
+// partials for each workgroup, 256 of them from 256 rows on.)
+constexpr int64_t kLnDirectRows = 512, kLnDirectValues = 3 << 21;
+constexpr int64_t kGatedDirectRows = 192, kDropDirectRows = 640, kDropDirectValues = 1 << 22;
 
 // R teams of a row's threads; LDS for their sums, or for the sums of workgroups that only sum.
 template <bool BF16, bool WBF, int C>
@@ -342,7 +340,7 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
   if (R > (M + kCUs - 1) / kCUs) R = (M + kCUs - 1) / kCUs;
   const int64_t G = even_grid((M + R - 1) / R, kCUs);
   // a dx in the place of dy or h would be written while the column sums read them
-  const bool direct = ln_direct(M, K) && dx != dy && dx != h;
+  const bool direct = M <= kLnDirectRows && M * K <= kLnDirectValues && dx != dy && dx != h;
   float* part = nullptr;
   if (!direct) {
     s = get_partials(st, G * 2 * K, &part);
