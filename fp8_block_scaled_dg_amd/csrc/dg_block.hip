@@ -136,19 +136,19 @@ dg_status launch_gated_ring(int bm, int64_t S, const Problem& p, const Epilogue&
   return launch_gated_ring_as<GatedCfg<2, 2, 2, PACKED, STREAM_B>>(p, S, ep, st);
 }
 
-// Estimated times in us, fitted to measurements on one MI355X: 390 products of 1 to 2048 rows, 256
+// Estimated times in us, fitted to measurements on one MI355X: 530 products of 1 to 2048 rows, 256
 // to 18432 columns of h, K = 512 to 18432, the kernels' every form that fits (bm rows, S splits),
 // most of them with so many weights in turn that each came from HBM. On them the choice is within
-// 1 % of the best form measured on average, within 10 % on all but a dozen (the worst, 1500 x 256 x
+// 1.1 % of the best form measured on average, within 10 % on all but 16 (the worst, 1500 x 256 x
 // 2048: 15 - 29 %).
 //   ring: launch, prologue and epilogue; the run's pairs; B's bytes; further rounds of tiles; for
 //   S > 1 the partials' trip through memory and the last split's sum over them.
 //   us by S:            1     2     3     4     6     8    14
-//    M = 1,  I = 2048, K = 7168, bm = 16   37.8  23.3  18.9  15.5  14.0  13.2  14.4  (tiles 25.6)
-//    M = 64, I = 2048, K = 7168, bm = 64   47.1  30.0  25.2  21.6  20.0  19.9  24.1  (28.3)
-//    M = 64, I = 8192, K = 8192, bm = 64   56.8  41.5  33.1  32.4                    (54.1)
-//    M = 1000, I = 2048, K = 7168          46.5 (bm = 32: 76)                        (49.4)
-//    M = 2048, I = 2816, K = 4096          82.1                                      (68.9)
+//    M = 1,  I = 2048, K = 7168, bm = 16   38.1  23.4  19.0  15.7  13.8  13.1  13.7  (tiles 25.6)
+//    M = 64, I = 2048, K = 7168, bm = 64   46.6  29.5  24.8  21.2  19.8  20.3  23.9  (28.3)
+//    M = 64, I = 8192, K = 8192, bm = 64   55.3  40.6  32.2  31.9                    (62.9)
+//    M = 1000, I = 2048, K = 7168          44.0 - 45.8 (bm = 32: 76)                 (46.6 - 47.5)
+//    M = 2048, I = 2816, K = 4096          76.9                                      (70.3)
 struct GatedPlan {
   int bm;  // 0: the tile kernel
   int64_t S;
@@ -174,9 +174,11 @@ GatedPlan gated_ring_plan(int bm, int64_t M, int64_t I, int64_t K) {
 double gated_pipe_time(int64_t M, int64_t I, int64_t K) {
   const int64_t KB = K / kKBlock, tiles = (M + 127) / 128 * (I / 128);
   const TailSplit ts = pipe_tail_split(tiles, KB);
-  const double round = 0.79 * (double)KB + 9.1, fixed = (double)(2 * I) * (double)K / 9.5e6 - 1.6;
+  const double round = 0.83 * (double)KB + 8.6, fixed = (double)(2 * I) * (double)K / 14.9e6 - 1.0;
   if (ts.parts == 1) return fixed + (double)((tiles + kCUs - 1) / kCUs) * round;
-  return fixed + (double)(ts.full / kCUs) * round + 0.79 * (double)(KB / ts.parts) + 12.6 + 1.2 * (double)ts.parts;
+  const double filled = (double)((tiles - ts.full) * ts.parts) / kCUs;  // of the last round
+  return fixed + (double)(ts.full / kCUs) * round + 0.83 * (double)(KB / ts.parts) + 9.2 + (double)ts.parts +
+         11.3 * filled;
 }
 
 // The tile kernel's 32-bit offsets reach from a gate row to its up row.

@@ -22,12 +22,17 @@
 // The second block of an odd run's last pair is zeroed the same way, A, B and scales, by offsets
 // out of range in the lanes that would bring it.
 //
-// What bounds it: one CU takes in about 62 KB/us by LDS DMA, from L2 or HBM, with two or three
-// chunks in flight alike, in 128- or 256-byte pieces (M = 1000, I = 2048, K = 7168, one tile per CU:
-// 46 us; the DMAs alone, without reads and MFMAs, 43), and HBM gives all CUs together 5.2 TB/s
-// (64 x 18432 x 7168, 264 MB of B: 56.8 us; 1 x 18432 x 7168: 48.1). B in registers, 64 bytes of 16
-// rows per load, took 70 us for the first and 80 for the second; four waves of 64 x 64 of each half
-// 52.7 and 58.5.
+// A chunk's DMAs are issued one or two at a time behind the MFMAs between two barriers; all at
+// once behind the barrier, M = 1000, I = 2048, K = 7168 took 45.1 us instead of 44.1, 512 rows 31.0
+// instead of 30.3 (one row the same).
+//
+// What bounds it: with B beyond its L2, a CU takes in about 62 KB/us by LDS DMA, which is 64 KB
+// in flight at 1.1 us, however deep the ring, in 128- or 256-byte pieces (that product, one tile per
+// CU: 44.1 us; the DMAs alone, without reads and MFMAs, 43; with B's lines in L2 36), and HBM gives all
+// CUs together 5.2 TB/s (64 x 18432 x 7168, 264 MB of B: 56.3 us; 1 x 18432 x 7168: 48.0). B in
+// registers, 64 bytes of 16 rows per load, took 70 us for the first and 80 for the second; four waves of
+// 64 x 64 of each half 52.7 and 58.5. A product of one row (1 x 2048 x 7168, 29 MB: 13.1 us at 5.7 for
+// the bytes) waits for the launch, the first bytes and the splits' trip through memory.
 //
 // S > 1 K splits: fp32 partials (rows below M only) and an arrival count per tile; the last
 // split to arrive adds all of them in split order (splitk_arrive), so results are deterministic.
@@ -87,34 +92,38 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gated_rsrc(const uint8_t* p, u
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, live ? (int)bytes : 0, 0x00020000);
 }
 
-// Chunk of pair t: gate (UP false: with A's pair and the scales) or up rows, into slot I.
-template <class Cfg, bool UP, int I, int T>
+// DMAs [LO, HI) of the chunk of pair t, into slot I: the gate rows' (UP false: the scales first,
+// then A's pair into slot T of its ring, then B) or the up rows'.
+template <class Cfg, bool UP, int I, int T, int LO, int HI>
 __device__ __forceinline__ void gated_issue(const GatedSrc<Cfg>& src, int t) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef __attribute__((address_space(3))) void* lds_ptr;
   constexpr int kPolicyB = Cfg::STREAM_B ? 2 : 0;  // 2: non-temporal
+  constexpr int B0 = UP ? 0 : 1 + Cfg::A_DMA;      // first DMA of B
   t = __builtin_amdgcn_readfirstlane(t);
   const bool live = t < src.pairs, half = src.odd && t == src.pairs - 1;
   const uint32_t skip[2] = {half ? src.second : 0, half ? src.second ^ 0x80000000u : 0};
-  if constexpr (!UP) {
-    uint8_t* st = gated_a<Cfg::A_STAGE, T>;
-    const int kb = src.kb0 + 2 * t;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        gated_rsrc(src.s, src.s_bytes, live),
-        (lds_ptr)(st + Cfg::OFF_S + (src.wave < 4 ? src.wave : 4) * 256), 4,
-        src.s_off | (half ? src.s_second : 0), (kb >> src.s_shift) << 2, 0, 0);
-    const __amdgpu_buffer_rsrc_t ra = gated_rsrc(src.a, src.a_bytes, live);
+  uint8_t* st = gated_a<Cfg::A_STAGE, T>;
+  const __amdgpu_buffer_rsrc_t ra = gated_rsrc(src.a, src.a_bytes, live);
+  const __amdgpu_buffer_rsrc_t rb = gated_rsrc(UP ? src.up : src.gate, src.b_bytes, live);
 #pragma unroll
-    for (int q = 0; q < Cfg::A_DMA; ++q)
+  for (int op = LO; op < HI; ++op) {
+    if (!UP && op == 0) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          gated_rsrc(src.s, src.s_bytes, live),
+          (lds_ptr)(st + Cfg::OFF_S + (src.wave < 4 ? src.wave : 4) * 256), 4,
+          src.s_off | (half ? src.s_second : 0), ((src.kb0 + 2 * t) >> src.s_shift) << 2, 0, 0);
+    } else if (op < B0) {
+      const int q = op - 1;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(st + (src.wave * Cfg::A_DMA + q) * 1024), 16,
                                                src.a_off[q] | skip[((src.wave * Cfg::A_DMA + q) >> 1) & 1],
                                                t * Cfg::ROW, 0, 0);
+    } else {
+      const int q = op - B0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(gated_chunk<I> + (src.wave * Cfg::B_DMA + q) * 1024),
+                                               16, src.b_off[q] | skip[(q >> 1) & 1], t * Cfg::ROW, 0, kPolicyB);
+    }
   }
-  const __amdgpu_buffer_rsrc_t rb = gated_rsrc(UP ? src.up : src.gate, src.b_bytes, live);
-#pragma unroll
-  for (int q = 0; q < Cfg::B_DMA; ++q)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(gated_chunk<I> + (src.wave * Cfg::B_DMA + q) * 1024),
-                                             16, src.b_off[q] | skip[(q >> 1) & 1], t * Cfg::ROW, 0, kPolicyB);
 #endif
 }
 
@@ -160,27 +169,52 @@ __device__ __forceinline__ void gated_read_b(v8i (&f)[Cfg::TN], int wave, int h,
   for (int j = 0; j < Cfg::TN; ++j) f[j] = gated_frag(gated_chunk<I>, (wn * Cfg::TN + j) * 16 + l16, h, g);
 }
 
-// acc += a b sa sb for one block.
-template <class Cfg>
-__device__ __forceinline__ void gated_mma(v4f (&acc)[Cfg::TM][Cfg::TN], const v8i (&a)[Cfg::TM],
-                                          const v8i (&b)[Cfg::TN], const float (&sa)[Cfg::TM], float sb) {
-#pragma unroll
-  for (int i = 0; i < Cfg::TM; ++i) {
-    const float s = sa[i] * sb;
-#pragma unroll
-    for (int j = 0; j < Cfg::TN; ++j) {
-      const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          b[j], a[i], v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(part[q], s, acc[i][j][q]);
-    }
+// acc += a b sa sb for one block, with the DMAs of issue.template op<n>() behind MFMA n, and a tile's
+// promotion behind the next tile's.
+template <class Cfg, int N, class Issue>
+__device__ __forceinline__ void gated_mma_from(v4f (&acc)[Cfg::TM][Cfg::TN], const v8i (&a)[Cfg::TM],
+                                               const v8i (&b)[Cfg::TN], const float (&s)[Cfg::TM], v4f before,
+                                               const Issue& issue) {
+  constexpr int TN = Cfg::TN, TILES = Cfg::TM * TN;
+  v4f part = before;
+  if constexpr (N < TILES) {
+    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[N % TN], a[N / TN], v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
+                                                            0, 0, 0);
+    issue.template op<N>();
   }
-  // the promotion stays in the MFMAs' basic block (ring_block says why)
+  if constexpr (N > 0) {
+    constexpr int I = (N - 1) / TN, J = (N - 1) % TN;
 #pragma unroll
-  for (int i = 0; i < Cfg::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < Cfg::TN; ++j) asm volatile("" : "+v"(acc[i][j]));
+    for (int q = 0; q < 4; ++q) acc[I][J][q] = __builtin_fmaf(before[q], s[I], acc[I][J][q]);
+    // the promotion stays in the MFMAs' basic block (ring_block says why)
+    asm volatile("" : "+v"(acc[I][J]));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (N < TILES) gated_mma_from<Cfg, N + 1>(acc, a, b, s, part, issue);
 }
+
+template <class Cfg, class Issue>
+__device__ __forceinline__ void gated_mma(v4f (&acc)[Cfg::TM][Cfg::TN], const v8i (&a)[Cfg::TM],
+                                          const v8i (&b)[Cfg::TN], const float (&sa)[Cfg::TM], float sb,
+                                          const Issue& issue) {
+  float s[Cfg::TM];
+#pragma unroll
+  for (int i = 0; i < Cfg::TM; ++i) s[i] = sa[i] * sb;
+  gated_mma_from<Cfg, 0>(acc, a, b, s, v4f{0.f, 0.f, 0.f, 0.f}, issue);
+}
+
+// The DMAs of a chunk over the MFMAs of two blocks (HALF 0, 1), between one barrier and the next.
+template <class Cfg, bool UP, int I, int T, int HALF>
+struct GatedIssue {
+  const GatedSrc<Cfg>& src;
+  int t;
+  template <int N>
+  __device__ __forceinline__ void op() const {
+    constexpr int TILES = Cfg::TM * Cfg::TN, OPS = UP ? Cfg::OPS_UP : Cfg::OPS_GATE;
+    gated_issue<Cfg, UP, I, T, (HALF * TILES + N) * OPS / (2 * TILES), (HALF * TILES + N + 1) * OPS / (2 * TILES)>(
+        src, t);
+  }
+};
 
 // Wait until at most N of this wave's DMAs are in flight and its LDS reads are done, then the
 // workgroup's barrier.
@@ -193,7 +227,8 @@ __device__ __forceinline__ void gated_sync() {
 }
 
 // Pair t, T = t % 3: chunks 2 t and 2 t + 1 in slots 2 T % 3 and (2 T + 1) % 3, A in slot T. `a`
-// holds the pair's A and `b0` the gate chunk's first block on entry, the next pair's on exit.
+// holds the pair's A and `b0` the gate chunk's first block on entry, the next pair's on exit. The
+// gate chunk of pair t + 1 is half issued on entry, that of pair t + 2 on exit.
 template <class Cfg, int T>
 __device__ __forceinline__ void gated_pair(v4f (&gate)[Cfg::TM][Cfg::TN], v4f (&up)[Cfg::TM][Cfg::TN],
                                            GatedA<Cfg>& a, v8i (&b0)[Cfg::TN], const GatedSrc<Cfg>& src,
@@ -204,22 +239,20 @@ __device__ __forceinline__ void gated_pair(v4f (&gate)[Cfg::TM][Cfg::TN], v4f (&
   v8i b1[Cfg::TN];
   gated_read_b<Cfg, G>(b1, src.wave, 1, g, l16);
   __builtin_amdgcn_sched_barrier(0);
-  gated_mma<Cfg>(gate, a.f[0], b0, a.s[0], g0);
+  gated_mma<Cfg>(gate, a.f[0], b0, a.s[0], g0, GatedIssue<Cfg, false, NEXT, (T + 1) % 3, 1>{src, t + 1});
   gated_sync<Cfg::OPS_GATE>();
-  gated_issue<Cfg, true, G, 0>(src, t + 1);
   gated_read_b<Cfg, U>(b0, src.wave, 0, g, l16);
   __builtin_amdgcn_sched_barrier(0);
-  gated_mma<Cfg>(gate, a.f[1], b1, a.s[1], g1);
+  gated_mma<Cfg>(gate, a.f[1], b1, a.s[1], g1, GatedIssue<Cfg, true, G, 0, 0>{src, t + 1});
   gated_read_b<Cfg, U>(b1, src.wave, 1, g, l16);
   __builtin_amdgcn_sched_barrier(0);
-  gated_mma<Cfg>(up, a.f[0], b0, a.s[0], u0);
+  gated_mma<Cfg>(up, a.f[0], b0, a.s[0], u0, GatedIssue<Cfg, true, G, 0, 1>{src, t + 1});
   gated_sync<Cfg::OPS_UP>();
-  gated_issue<Cfg, false, U, (T + 2) % 3>(src, t + 2);
   GatedA<Cfg> next;
   next.template read<(T + 1) % 3>(src, t + 1, g, l16);
   gated_read_b<Cfg, NEXT>(b0, src.wave, 0, g, l16);
   __builtin_amdgcn_sched_barrier(0);
-  gated_mma<Cfg>(up, a.f[1], b1, a.s[1], u1);
+  gated_mma<Cfg>(up, a.f[1], b1, a.s[1], u1, GatedIssue<Cfg, false, U, (T + 2) % 3, 0>{src, t + 2});
   a = next;
 }
 
@@ -290,10 +323,10 @@ __global__ void __launch_bounds__(512) gated_ring_kernel(GatedArgs args) {
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) gate[i][j] = up[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  gated_issue<Cfg, false, 0, 0>(src, 0);
-  gated_issue<Cfg, true, 1, 0>(src, 0);
-  gated_issue<Cfg, false, 2, 1>(src, 1);
-  gated_sync<Cfg::OPS_UP + Cfg::OPS_GATE>();
+  gated_issue<Cfg, false, 0, 0, 0, Cfg::OPS_GATE>(src, 0);
+  gated_issue<Cfg, true, 1, 0, 0, Cfg::OPS_UP>(src, 0);
+  gated_issue<Cfg, false, 2, 1, 0, Cfg::OPS_GATE / 2>(src, 1);  // as a pair's last block leaves it
+  gated_sync<Cfg::OPS_UP + Cfg::OPS_GATE / 2>();
   GatedA<Cfg> a;
   v8i b0[TN];
   a.template read<0>(src, 0, g, l16);
@@ -350,8 +383,9 @@ __global__ void __launch_bounds__(512) gated_ring_kernel(GatedArgs args) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) sum[0][i][j] = sum[1][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    // four splits' partials in flight at a time (this split's is in registers)
-    constexpr int F = 4;
+    // eight or four splits' partials in flight at a time, 64 or 128 registers (this split's own are
+    // there already); with four, a product of one row took 0.7 us longer
+    constexpr int F = TM * TN == 1 ? 8 : 4;
     for (int s0 = 0; s0 < S; s0 += F) {
       v4u part[F][2][TM][TN];
 #pragma unroll
