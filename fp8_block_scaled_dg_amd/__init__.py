@@ -1,9 +1,9 @@
 """Python binding of libdg.so, the MI355X (gfx950) FP8 block-scaled GEMM library.
 
-Argument marshalling only (in part native, csrc/marshal.cpp): every call checks dtypes, devices, shapes and contiguity,
-then passes raw device pointers and torch's current HIP stream to the C ABI declared
-in ``include/dg.h``. All arithmetic runs in the library's HIP kernels; there is no
-fallback path. If libdg.so is missing the import fails.
+Argument marshalling only (of the newer calls natively, csrc/marshal.cpp): every call
+checks dtypes, devices, shapes and contiguity, then passes raw device pointers and torch's
+current HIP stream to the C ABI declared in ``include/dg.h``. All arithmetic runs in the
+library's HIP kernels; there is no fallback path. If libdg.so is missing the import fails.
 
 Calls (DeepGEMM project page, aiproducthub.cn, "quick start"; DeepGEMM launch
 article, deepseek.csdn.net, section 4.2 "advanced tuning"):

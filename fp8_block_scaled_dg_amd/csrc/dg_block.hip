@@ -3,11 +3,11 @@
 // dropout, and their backward passes. Argument checks, choice of a kernel form, launches.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 
 #include "../../include/dg.h"
 #include "dropout.hpp"
@@ -59,15 +59,17 @@ dg_status launch_layernorm_backward(const LayerNormBwdArgs& a, unsigned grid, un
                                     hipStream_t st) {
   const auto kernel = layernorm_backward_kernel<BF16, WBF, C>;
   constexpr bool lds_dw = kLnLdsDw<BF16, C>;
-  if (lds_dw) {  // up to 128 KB
-    static std::once_flag once;
-    static hipError_t attr_err = hipSuccess;
-    std::call_once(once, [&] {
-      attr_err = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     kNormMaxK * (int)sizeof(float));
-    });
-    if (attr_err != hipSuccess)
-      return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(attr_err));
+  if (lds_dw) {  // up to 128 KB, an attribute of the kernel on each device
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (e == hipSuccess && (dev > 63 || !(done.load() & bit))) {
+      e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                              kNormMaxK * (int)sizeof(float));
+      if (e == hipSuccess && dev <= 63) done.fetch_or(bit);
+    }
+    if (e != hipSuccess) return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(e));
   }
   size_t bytes = (size_t)(lds_dw ? a.K : (a.teams - 1) * a.K) * sizeof(float);
   const size_t direct = (size_t)threads * 2 * Pieces<BF16>::P * sizeof(float);
@@ -352,9 +354,7 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
                            (int32_t)R, (int32_t)G};
   const unsigned grid = (unsigned)(G + (direct ? K / kLnDirectCols : 0));
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    s = no_throw([&] {
-      return launch_layernorm_backward<xb.value, wb.value, c.value>(a, grid, (unsigned)(nt * R), st);
-    });
+    s = launch_layernorm_backward<xb.value, wb.value, c.value>(a, grid, (unsigned)(nt * R), st);
   });
   if (s != DG_OK) return s;
   s = launched("layernorm_backward_kernel");
