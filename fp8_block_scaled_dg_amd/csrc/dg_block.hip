@@ -36,22 +36,27 @@ dg_status drop_args(double p, const int64_t* rng, int64_t subsequence, DropArgs*
 
 // ---------------------------------------------------------------- column sums in one launch
 //
-// Up to these sizes the backward kernels sum columns in the same launch, in extra workgroups that
-// read the inputs a second time. Us in a graph, so many buffers in turn that they come from HBM, one
-// launch against two:
+// Up to these sizes the backward kernels sum columns in the same launch, in further workgroups, ahead
+// of the others, that read the inputs a second time. Us in a graph, so many buffers in turn that they
+// come from HBM, one launch against two:
 //             layer norm bf16         gated (gelu)            dropout fp32
-//    130 x 2048   4.9,  7.0             6.9,  7.5               3.3, 6.0
-//    256 x 2048   5.6,  8.2             8.4,  8.0               4.3, 6.3
-//    512 x 2048   8.3,  9.4            13.9,  9.2               6.3, 6.8
-//    700 x 2048  12.4,  9.9            17.8, 10.8               8.2, 7.6
-//    130 x 7168   7.9, 11.6             8.3,  9.2               4.8, 6.7
-//    256 x 7168   9.8, 16.0            12.3, 11.5               5.8, 8.3
-//    512 x 7168  14.4, 17.7            19.9, 14.8               9.0, 10.0
-//    700 x 7168  17.3, 19.0            26.7, 19.3              12.9, 11.9
-// and the layer norm's gradient of 512 x 16384 fp32 41.2, 38.2. (Its two launches move 4 K bytes of
-// partials for each workgroup, 256 of them from 256 rows on.)
-constexpr int64_t kLnDirectRows = 512, kLnDirectValues = 3 << 21;
-constexpr int64_t kGatedDirectRows = 192, kDropDirectRows = 640, kDropDirectValues = 1 << 22;
+//    130 x 2048   4.8,  6.9             6.0,  7.4               3.3,  6.0
+//    257 x 2048   6.2,  7.8             8.1,  8.0               4.9,  6.2
+//    512 x 2048   8.1,  9.4            11.4,  9.2               5.9,  6.8
+//    700 x 2048  10.2, 10.0            13.8, 10.7               7.9,  7.6
+//    130 x 7168   6.3, 11.6             6.8,  9.2               4.6,  6.7
+//    257 x 7168   8.7, 12.9            10.9, 11.4               5.8,  8.2
+//    512 x 7168  12.1, 17.5            17.6, 14.6               8.4,  9.9
+//    700 x 7168  15.6, 19.0            20.6, 19.3              11.1, 11.9
+//   1000 x 7168  21.0, 21.9            27.9, 23.2              14.3, 14.1
+//    130 x 16384 14.3, 16.5            11.8, 12.1               5.9,  8.5
+//    200 x 16384 15.9, 22.4            16.1, 14.9               7.9, 10.0
+//    512 x 16384 27.0, 27.9            33.5, 25.0              16.4, 15.8
+// (The layer norm's two launches move 8 K bytes of partials for each workgroup, 256 of them from 256
+// rows on.)
+constexpr int64_t kLnDirectValues = 1 << 23, kGatedDirectRows = 256, kGatedDirectValues = 1 << 21;
+constexpr int64_t kDropDirectRows = 640, kDropDirectValues = 3 << 21;
+int64_t ln_direct_rows(int64_t K) { return 384 + K / 16; }
 
 // R teams of a row's threads; LDS for their sums, or for the sums of workgroups that only sum.
 template <bool BF16, bool WBF, int C>
@@ -344,7 +349,7 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
   if (R > (M + kCUs - 1) / kCUs) R = (M + kCUs - 1) / kCUs;
   const int64_t G = even_grid((M + R - 1) / R, kCUs);
   // a dx in the place of dy or h would be written while the column sums read them
-  const bool direct = M <= kLnDirectRows && M * K <= kLnDirectValues && dx != dy && dx != h;
+  const bool direct = M <= ln_direct_rows(K) && M * K <= kLnDirectValues && dx != dy && dx != h;
   float* part = nullptr;
   if (!direct) {
     s = get_partials(st, G * 2 * K, &part);
@@ -417,7 +422,7 @@ dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activat
   const hipStream_t st = (hipStream_t)stream;
   if (M == 0) return dbias ? launch_column_sum(nullptr, dbias, 0, 2 * I, st) : DG_OK;
   const StripPlan pl = strip_plan(M, I);
-  const bool direct = dbias && M <= kGatedDirectRows && M * I <= kDirectActValues, sum = dbias && !direct;
+  const bool direct = dbias && M <= kGatedDirectRows && M * I <= kGatedDirectValues, sum = dbias && !direct;
   float* part = nullptr;
   if (sum) {
     s = get_partials(st, pl.groups * 2 * I, &part);

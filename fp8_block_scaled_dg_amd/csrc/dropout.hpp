@@ -134,14 +134,7 @@ struct DropAddArgs {
 constexpr int kDropThreads = 256, kDropUnroll = 2;
 constexpr int64_t kDropChunk = 512;  // values that a wave takes per step
 
-// 16 bytes of type BF16 as fp32 and back.
-template <bool BF16>
-__device__ __forceinline__ void unpack_piece(const quant_v4u& u, float (&v)[Pieces<BF16>::P]) {
-#pragma unroll
-  for (int i = 0; i < Pieces<BF16>::P; ++i)
-    v[i] = __uint_as_float(!BF16 ? u[i & 3] : i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
-}
-
+// 16 bytes of type BF16 of fp32 values.
 template <bool BF16>
 __device__ __forceinline__ quant_v4u pack_piece(const float (&v)[Pieces<BF16>::P]) {
   if constexpr (BF16)
@@ -241,7 +234,7 @@ struct DropBwdArgs {
   uint8_t* codes;
   ScaleOut so;
   float* part;   // [row groups][K] partial dbias; NULL: none
-  float* dbias;  // part == NULL: written by workgroups from strips * groups on, if any
+  float* dbias;  // part == NULL: written by further workgroups, if any
   int64_t M;
   int64_t rows;  // rows per row group
   int32_t K;
@@ -257,20 +250,28 @@ __global__ void __launch_bounds__(256) dropout_backward_kernel(DropBwdArgs a) {
   __shared__ float sums[3][1024];
   const Drop drop(a.drop);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if ((int)blockIdx.x >= a.strips * a.groups) {
+  const int work = a.strips * a.groups, index = sums_first(work);
+  if (index >= work) {
     constexpr int P = Pieces<BF16>::P;
-    direct_sums<1, P, kDropDirectCols>(
-        a.M, ((int)blockIdx.x - a.strips * a.groups) * kDropDirectCols, {a.dbias}, &sums[0][0],
-        [&](int64_t m, int c, float (&v)[1][P]) {
+    struct Row {
+      quant_v4u dy;
+      int c;
+    };
+    direct_sums<1, P, kDropDirectCols, true>(
+        a.M, (index - work) * kDropDirectCols, {a.dbias}, &sums[0][0],
+        [&](int64_t m, int c) {
+          return Row{raw_piece<BF16>(a.dy, m * a.K + c), c};
+        },
+        [&](const Row& row, int64_t m, float (&v)[1][P]) {
           float d[P];
-          load_piece<BF16>(a.dy, m * a.K + c, d);
-          drop_piece<BF16>(drop, m * a.K + c, d);
+          unpack_piece<BF16>(row.dy, d);
+          drop_piece<BF16>(drop, m * a.K + row.c, d);
 #pragma unroll
           for (int i = 0; i < P; ++i) v[0][i] += d[i];
         });
     return;
   }
-  const int strip = blockIdx.x % a.strips, group = blockIdx.x / a.strips;
+  const int strip = index % a.strips, group = index / a.strips;
   const int in_strip = (lane >> 3) * 128 + (lane & 7) * Pieces<BF16>::P;
   const int col = strip * 1024 + in_strip;
   const int64_t m1 = min(a.M, (group + 1) * a.rows);

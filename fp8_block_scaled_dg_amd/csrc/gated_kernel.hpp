@@ -19,7 +19,7 @@ struct GatedBwdArgs {
   uint8_t* codes;
   ScaleOut so;
   float* part;   // [row groups][2 I] partial dbias; NULL: none
-  float* dbias;  // part == NULL: written by workgroups from strips * groups on, if any
+  float* dbias;  // part == NULL: written by further workgroups, if any
   int64_t M;
   int64_t rows;  // rows per row group
   int32_t I;
@@ -34,21 +34,29 @@ static __global__ void __launch_bounds__(256) gated_backward_kernel(GatedBwdArgs
   __shared__ float sums[3][2][1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t I = a.I, N = 2 * I;
-  if ((int)blockIdx.x >= a.strips * a.groups) {
-    direct_sums<2, 8, kGatedDirectCols>(
-        a.M, ((int)blockIdx.x - a.strips * a.groups) * kGatedDirectCols, {a.dbias, a.dbias + I}, &sums[0][0][0],
-        [&](int64_t m, int c, float (&v)[2][8]) {
+  const int work = a.strips * a.groups, index = sums_first(work);
+  if (index >= work) {
+    struct Row {
+      quant_v4u d, g, u;
+    };
+    direct_sums<2, 8, kGatedDirectCols, false>(
+        a.M, (index - work) * kGatedDirectCols, {a.dbias, a.dbias + I}, &sums[0][0][0],
+        [&](int64_t m, int c) {
+          return Row{raw_piece<true>(a.dh, m * I + c), raw_piece<true>(a.pre, m * N + c),
+                     raw_piece<true>(a.pre, m * N + I + c)};
+        },
+        [&](const Row& row, int64_t, float (&v)[2][8]) {
           float d[8], g[8], x[8];
-          load_piece<true>(a.dh, m * I + c, d);
-          load_piece<true>(a.pre, m * N + c, g);
-          load_piece<true>(a.pre, m * N + I + c, x);
+          unpack_piece<true>(row.d, d);
+          unpack_piece<true>(row.g, g);
+          unpack_piece<true>(row.u, x);
           gated_backward(d, g, x, a.act);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[0][i] += g[i], v[1][i] += x[i];
         });
     return;
   }
-  const int strip = blockIdx.x % a.strips, group = blockIdx.x / a.strips;
+  const int strip = index % a.strips, group = index / a.strips;
   const int in_strip = (lane >> 3) * 128 + (lane & 7) * Pieces<true>::P;
   const int col = strip * 1024 + in_strip;
   const int64_t m1 = min(a.M, (group + 1) * a.rows);

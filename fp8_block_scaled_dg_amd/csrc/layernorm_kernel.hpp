@@ -164,7 +164,7 @@ struct LayerNormBwdArgs {
   const float* mean;
   const float* rstd;
   void* dx;
-  float* part;     // [groups][2 K] partial dweight, dbias; NULL: workgroups from `groups` on sum them
+  float* part;     // [groups][2 K] partial dweight, dbias; NULL: further workgroups sum them
   float* dweight;  // part == NULL: the sums
   float* dbias;
   int64_t M;
@@ -199,18 +199,25 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
   extern __shared__ float lds[];  // [teams - 1][K], LDS_DW: [K]; or the direct sums'
   const int K = a.K, R = a.teams, threads = blockDim.x / R;
   const float inv_k = 1.f / (float)K;
-  if ((int)blockIdx.x >= a.groups) {
+  const int index = sums_first(a.groups);
+  if (index >= a.groups) {
     constexpr int P = Pieces<BF16>::P;
-    direct_sums<2, P, kLnDirectCols>(
-        a.M, ((int)blockIdx.x - a.groups) * kLnDirectCols, {a.dweight, a.dbias}, lds,
-        [&](int64_t m, int c, float (&v)[2][P]) {
+    struct Row {
+      quant_v4u dy, h;
+      float mean, rstd;
+    };
+    direct_sums<2, P, kLnDirectCols, true>(
+        a.M, (index - a.groups) * kLnDirectCols, {a.dweight, a.dbias}, lds,
+        [&](int64_t m, int c) {
+          return Row{raw_piece<BF16>(a.dy, m * K + c), raw_piece<BF16>(a.h, m * K + c), a.mean[m], a.rstd[m]};
+        },
+        [&](const Row& row, int64_t, float (&v)[2][P]) {
           float d[P], x[P];
-          load_piece<BF16>(a.dy, m * K + c, d);
-          load_piece<BF16>(a.h, m * K + c, x);
-          const float mean = a.mean[m], rstd = a.rstd[m];
+          unpack_piece<BF16>(row.dy, d);
+          unpack_piece<BF16>(row.h, x);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            v[0][i] = __builtin_fmaf(d[i], (x[i] - mean) * rstd, v[0][i]);
+            v[0][i] = __builtin_fmaf(d[i], (x[i] - row.mean) * row.rstd, v[0][i]);
             v[1][i] += d[i];
           }
         });
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
       if (AHEAD && col[c] < K && a.dh) dh[c].load(a.dh, m * K + col[c]);
   };
   const int64_t step = (int64_t)a.groups * R;
-  int64_t m = (int64_t)blockIdx.x * R + team;
+  int64_t m = (int64_t)index * R + team;
   if (AHEAD && m < a.M) {
     fetch(m);
     fetch_dh(m);
@@ -313,7 +320,7 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_backward_kernel(LayerN
     if (AHEAD && m + step < a.M) fetch_dh(m + step);
   }
   if (!a.part) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * K;
+  float* part = a.part + (int64_t)index * 2 * K;
   if constexpr (LDS_DW) {  // R = 1
 #pragma unroll
     for (int c = 0; c < C; ++c)
