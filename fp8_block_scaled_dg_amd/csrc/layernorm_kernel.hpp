@@ -17,6 +17,11 @@
 //   squares = sum over waves of squares_w + count_w (mean_w - mean)^2
 // (Chan, Golub, LeVeque, "Updating formulae and a pairwise algorithm for computing sample
 // variances", 1979).
+//
+// Measured: forward 4096 x 7168 bf16 with residual and dropout 37.5 us, 206 MB at 5.5 TB/s (a copy of
+// 1 GiB: 5.1), one row 3.3 us from start to end, most of it dependent steps; backward 4096 x 7168
+// bf16 with dh 45 us, 235 MB at 5.2 TB/s, and 4.8 for the column sums; 257 x 2048 fp32, one launch,
+// 4.0 us.
 #pragma once
 
 #include "dropout.hpp"
@@ -55,7 +60,8 @@ struct LayerNormArgs {
 
 // The rows and chunks of rmsnorm_kernel. KEEP: weights and bias stay in registers; otherwise
 // (long rows) they are loaded where they are used. AHEAD: the next row is loaded before the
-// barrier of this one, which only the longest fp32 rows leave no registers for.
+// barrier of this one, which only the longest fp32 rows leave no registers for (1000 x 32768 fp32:
+// 86 us).
 template <bool BF16, bool WBF, int C, bool DROP>
 __global__ void __launch_bounds__(kNormThreads) layernorm_kernel(LayerNormArgs a) {
   constexpr bool KEEP = C <= (BF16 ? 2 : 1), AHEAD = BF16 || C <= 3;
@@ -188,7 +194,7 @@ __device__ __forceinline__ void lds_add16(float* sums, const float (&v)[16]) {
 // The teams and chunks of rmsnorm_backward_kernel, with two sums per row and two per column.
 // LDS_DW: the sums of dweight lie in LDS, those of dbias in registers, which do not hold both
 // beside the values of a row in several chunks (registers alone spill 77 to 169 of them from
-// 16384 fp32 values on, 1000 x 18432: 121 us). AHEAD as there.
+// 16384 fp32 values on, 1000 x 18432: 121 us; 74 with LDS). AHEAD as there.
 template <bool BF16, int C>
 constexpr bool kLnLdsDw = C >= (BF16 ? 3 : 2);
 

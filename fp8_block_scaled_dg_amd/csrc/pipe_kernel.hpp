@@ -884,6 +884,9 @@ __device__ __forceinline__ void pipe_store_epi(const Problem& p, const TileView&
 // once, a row's 1x128 block of h is reduced by lane moves, and pre and the codes go out as whole
 // lines. 16-byte chunk c of a row's half sits at chunk (c / 2 + 16 (c % 2)) ^ (row % 32), which
 // lets 16 lanes reading their even (odd) chunks hit disjoint banks, and the writes too.
+// Bound as the plain tile: 4096 x 18432 x 7168 (K) in us: the plain product of both halves 1036, gated
+// with bias 1029, silu 1042, gelu 1067, silu and pre 1080, gelu and pre 1093; K = 2048, 4096 x 7168: 149,
+// 156, 161, 171, 162, 173.
 __device__ __forceinline__ uint8_t* pipe_gated_row(int row) {  // 48 rows a stage
   return row < 48 ? pipe_stage0 + row * 1024
                   : row < 96 ? pipe_stage1 + (row - 48) * 1024 : pipe_stage2 + (row - 96) * 1024;
