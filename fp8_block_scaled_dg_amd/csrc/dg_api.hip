@@ -91,8 +91,9 @@ dg_status launch_pipe_as(const Problem& p0, int64_t blocks, const Epilogue& ep,
   if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld tiles", (long long)grid);
   a.full_tiles = (int32_t)grid;
   a.parts = 1;
+  const TailSplit ts = KIND == kDense ? pipe_tail_split(grid, p.K / kKBlock) : TailSplit{grid, 1};
+  const StreamTurn turn(stream, ts.parts > 1);
   if (KIND == kDense) {
-    const TailSplit ts = pipe_tail_split(grid, p.K / kKBlock);
     if (ts.parts > 1) {
       const int64_t split = grid - ts.full;
       const size_t bytes = (size_t)(split * ts.parts) * Cfg::BM * Cfg::BN * sizeof(float);
@@ -382,6 +383,7 @@ dg_status launch_skinny(const Problem& p0, int64_t blocks, hipStream_t stream) {
   a.group = (LAY & kLayBN) ? tile_group(tiles) : 1;
   const int64_t grid = (LAY & kLayBN) ? 8 * tiles_per_xcd(tiles, 1) * S : tiles * S;
   if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld", (long long)grid);
+  const StreamTurn turn(stream, S > 1);
   if (S > 1) {
     const size_t part = (size_t)(tiles * S) * 64 * Cfg::BN * sizeof(float);
     dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
@@ -445,6 +447,7 @@ dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
   a.tiles = (int32_t)pl.tiles;
   a.group = (int32_t)pl.group;
   if (pl.grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld", (long long)pl.grid);
+  const StreamTurn turn(stream, pl.S > 1);
   if (pl.S > 1) {
     const size_t part = (size_t)(pl.tiles * pl.S) * 64 * Cfg::BN * sizeof(float);
     dg_status st = get_workspace(stream, part, (size_t)pl.tiles, &a.ws, &a.counters);
@@ -527,6 +530,7 @@ dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t strea
   const int64_t grid = tiles * pl.S;
   if (grid >= kLaunchThreads / Cfg::NT)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld workgroups", (long long)grid);
+  const StreamTurn turn(stream, pl.S > 1);
   if (pl.S > 1) {
     const size_t part = (size_t)grid * Cfg::BM * Cfg::BN * sizeof(float);
     const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
@@ -1159,6 +1163,7 @@ dg_status gemm_layout(const void* A, const void* B, void* C, const float* sfA,
   maybe_print(kDense, M, N, K, 1, id, a_t ? (b_n ? " (TN, transposed copy)" : " (TT, transposed copy)")
                                            : " (NN, transposed copy)");
   uint8_t *a2 = nullptr, *b2 = nullptr;
+  const StreamTurn turn(st);
   s = get_transpose_workspace(st, a_t ? (size_t)(M * K) : 0, b_n ? (size_t)(N * K) : 0, &a2, &b2);
   if (s != DG_OK) return s;
   if (a_t && (s = launch_transpose((const uint8_t*)A, a2, K, M, st)) != DG_OK) return s;
@@ -1425,6 +1430,7 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
   // a dx in the place of dy or h would be written while the column sums read them
   const bool direct = M <= kDirectRows && dx != dy && dx != h;
   float* part = nullptr;
+  const StreamTurn turn(st, !direct);
   if (!direct) {
     s = get_partials(st, G * K, &part);
     if (s != DG_OK) return s;
@@ -1460,6 +1466,7 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
   const StripPlan pl = strip_plan(M, N);
   const bool direct = dbias && M <= kDirectRows && M * N <= kDirectActValues, sum = dbias && !direct;
   float* part = nullptr;
+  const StreamTurn turn(st, sum);
   if (sum) {
     s = get_partials(st, pl.groups * N, &part);
     if (s != DG_OK) return s;

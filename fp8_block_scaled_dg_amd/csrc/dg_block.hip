@@ -97,6 +97,7 @@ dg_status launch_pipe_gated(const Problem& p0, const Epilogue& ep, hipStream_t s
   a.full_tiles = (int32_t)grid;
   a.parts = 1;
   const TailSplit ts = pipe_tail_split(grid, p0.K / kKBlock);
+  const StreamTurn turn(stream, ts.parts > 1);
   if (ts.parts > 1) {
     const int64_t split = grid - ts.full;
     const size_t bytes = (size_t)(split * ts.parts) * Cfg::BM * Cfg::BN * sizeof(float);
@@ -127,6 +128,7 @@ dg_status launch_gated_ring_as(const Problem& p, int64_t S, const Epilogue& ep, 
   const int64_t grid = tiles * S;
   if (grid >= kLaunchThreads / Cfg::NT)
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld workgroups", (long long)grid);
+  const StreamTurn turn(stream, S > 1);
   if (S > 1) {
     const size_t part = (size_t)grid * 2 * Cfg::BM * 128 * sizeof(float);
     const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
@@ -279,6 +281,7 @@ dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropo
   const StripPlan pl = strip_plan(M, K);
   const bool direct = dbias && M <= kDropDirectRows && M * K <= kDropDirectValues, sum = dbias && !direct;
   float* part = nullptr;
+  const StreamTurn turn(st, sum);
   if (sum) {
     s = get_partials(st, pl.groups * K, &part);
     if (s != DG_OK) return s;
@@ -351,6 +354,7 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
   // a dx in the place of dy or h would be written while the column sums read them
   const bool direct = M <= ln_direct_rows(K) && M * K <= kLnDirectValues && dx != dy && dx != h;
   float* part = nullptr;
+  const StreamTurn turn(st, !direct);
   if (!direct) {
     s = get_partials(st, G * 2 * K, &part);
     if (s != DG_OK) return s;
@@ -424,6 +428,7 @@ dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activat
   const StripPlan pl = strip_plan(M, I);
   const bool direct = dbias && M <= kGatedDirectRows && M * I <= kGatedDirectValues, sum = dbias && !direct;
   float* part = nullptr;
+  const StreamTurn turn(st, sum);
   if (sum) {
     s = get_partials(st, pl.groups * 2 * I, &part);
     if (s != DG_OK) return s;

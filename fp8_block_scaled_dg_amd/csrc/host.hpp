@@ -6,6 +6,7 @@
 
 #include <cstdint>
 #include <exception>
+#include <mutex>
 #include <type_traits>
 
 #include "../../include/dg.h"
@@ -35,6 +36,29 @@ inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)
 
 inline bool known_dtype(int32_t t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
 inline bool known_act(int32_t a) { return a >= DG_ACT_NONE && a <= DG_ACT_GELU_TANH; }
+
+// Held from where a call takes its stream's buffers to its last launch that uses them, so that
+// calls of several threads on one stream do not launch in between (a backward call's partial sums
+// and their sum are two launches, and the partials of any K split lie in the same buffer). A mutex
+// for every 64th of the streams; recursive, since a call on transposed copies makes another.
+class StreamTurn {
+ public:
+  explicit StreamTurn(hipStream_t stream, bool needed = true) : mu_(needed ? &slot(stream) : nullptr) {
+    if (mu_) mu_->lock();
+  }
+  ~StreamTurn() {
+    if (mu_) mu_->unlock();
+  }
+  StreamTurn(const StreamTurn&) = delete;
+  StreamTurn& operator=(const StreamTurn&) = delete;
+
+ private:
+  static std::recursive_mutex& slot(hipStream_t stream) {
+    static std::recursive_mutex slots[64];
+    return slots[((uintptr_t)stream >> 6) & 63];
+  }
+  std::recursive_mutex* mu_;
+};
 
 // f(), a C++ exception of the host code (std::bad_alloc of the workspace tables) turned into
 // a status: none leaves a C entry.

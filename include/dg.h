@@ -29,8 +29,8 @@
  *        larger dense GEMM);
  *      - transposed operand copies, for the NN / TN / TT calls;
  *      - fp32 partial column sums (in the partial tiles' buffer), for the backward calls.
- *    Calls on one stream share them in stream order; calls on different streams
- *    never share them. The buffers only grow. An outgrown buffer is retired, not
+ *    Calls on one stream share them in stream order, also where several threads make
+ *    them at once; calls on different streams never share them. The buffers only grow. An outgrown buffer is retired, not
  *    freed: it stays allocated until dg_release_workspaces() or the end of the
  *    process, so a HIP graph captured before the growth still finds its buffers.
  *  - HIP graph capture: a call that needs no larger buffer allocates nothing, so a

@@ -120,6 +120,52 @@ def test_two_streams_at_once():
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
 
 
+def test_threads_on_one_stream():
+    # gradients of two launches (partial sums, then their sum) and a product that splits K: all of
+    # them use the stream's one buffer of partials
+    m = dg()
+    stream = torch.cuda.Stream()
+    K = 1024
+    w = torch.ones(K, dtype=BF, device="cuda")
+    data, want = [], []
+    for i, M in enumerate((900, 1500)):
+        h, dy = inputs(M, K, 20 + i)
+        data.append((dy, h, w, torch.zeros(M, device="cuda"), torch.ones(M, device="cuda")))
+        want.append(m.layernorm_backward(*data[i]))
+    a, b = signs(5, 64, 7168), signs(6, 2112, 7168)
+    sa, sb, c0 = torch.ones(64, 56, device="cuda"), torch.ones(17, 56, device="cuda"), \
+        torch.empty(64, 2112, dtype=BF, device="cuda")
+    m.fp8_gemm_nt(a, b, c0, sa, sb)
+    torch.cuda.synchronize()
+    got, errors = [[], [], []], []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(100):
+                    if i < 2:
+                        got[i].append(m.layernorm_backward(*data[i]))
+                    else:
+                        c = torch.empty_like(c0)
+                        m.fp8_gemm_nt(a, b, c, sa, sb)
+                        got[i].append(c)
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for i in range(2):
+        assert len(got[i]) == 100
+        for g in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(g, want[i])), i
+    assert len(got[2]) == 100 and all(torch.equal(c, c0) for c in got[2])
+
+
 def test_python_checks_and_native_ones_pass_the_same_calls(monkeypatch):
     m = dg()
     ex = example()
