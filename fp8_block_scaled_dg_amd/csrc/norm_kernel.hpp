@@ -270,7 +270,7 @@ __device__ __forceinline__ int sums_first(int work) {
   return b < sums ? work + b : b - sums;
 }
 
-// The same for NS sums of each of COLS columns, to out[0 .. NS - 1] (NULL: not stored), with four
+// direct_column_sums with NS sums of each of COLS columns, to out[0 .. NS - 1] (NULL: not stored), four
 // rows' loads in flight: load(m, col) gives a row's values, add(row, m, v) adds them to
 // v[0 .. NS - 1]. sums: LDS for NS * P floats of every thread. WHOLE: no test lies between the rows
 // of a whole batch of four, so that their arithmetic overlaps; 512 x 2048 fp32 of dropout's gradient

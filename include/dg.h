@@ -452,7 +452,7 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
  *   sfB   fp32 [2 I / 128][K/128];  bias [2 I] fp32 or bf16 (bias_dtype), NULL: none
  *   codes e4m3fn [M][I];  sf fp32 [M][I/128] or (sf_packed) uint32 [M][ceil(I/512)]
  *   pre   bf16 [M][2 I] = z, for dg_gated_backward_fp8; NULL: not stored
- * I % 128 == 0, I <= 2^29, K <= 2^22, I * K < 2^42; alignment, stream, workspace and error rules of
+ * I % 128 == 0, I <= 2^29, M <= 2^30, K <= 2^22, I * K < 2^42; alignment, stream, workspace and error rules of
  * dg_fp8_gemm_nt_bias_act_fp8. Codes and scales of a block holding an infinity or NaN are
  * unspecified.
  */
