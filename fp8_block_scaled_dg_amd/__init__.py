@@ -138,10 +138,6 @@ lib.dg_dropout_backward_fp8.restype = ctypes.c_int
 lib.dg_dropout_backward_fp8.argtypes = [_vp, _i32, ctypes.c_double, _vp, _i64, _vp, _vp, _i32, _vp, _i64,
                                         _i64, _vp]
 
-_marshal.bind(*(ctypes.cast(f, _vp).value for f in (
-    lib.dg_layernorm_fp8_1x128, lib.dg_layernorm_backward, lib.dg_fp8_gemm_nt_gated_fp8,
-    lib.dg_gated_backward_fp8, lib.dg_dropout_add, lib.dg_dropout_backward_fp8)))
-
 lib.dg_release_workspaces.restype = ctypes.c_int
 lib.dg_release_workspaces.argtypes = []
 lib.dg_num_configs.restype = _i32
@@ -166,6 +162,11 @@ class DGError(RuntimeError):
 def check(status: int) -> None:
     if status != 0:
         raise DGError(status)
+
+
+_marshal.bind(*(ctypes.cast(f, _vp).value for f in (
+    lib.dg_layernorm_fp8_1x128, lib.dg_layernorm_backward, lib.dg_fp8_gemm_nt_gated_fp8,
+    lib.dg_gated_backward_fp8, lib.dg_dropout_add, lib.dg_dropout_backward_fp8)), check)
 
 
 def _fp8(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -584,9 +585,9 @@ def bias_act_backward_fp8(dc, pre=None, activation=None, codes=None, sf=None, db
     return codes, sf, dbias
 
 
-# The calls below first go through csrc/marshal.cpp, which returns None unless every argument is
-# as the call wants it and on the current GPU; the Python code behind it then raises the specific
-# error, or makes the call on another GPU. (layernorm_fp8_1x128 of one row takes the host 8.4 us
+# The calls below first go through csrc/marshal.cpp, which returns None, without having called the
+# library, unless every argument is as the call wants it and on the current GPU; the Python code
+# behind it then raises the specific error, or makes the call on another GPU. (layernorm_fp8_1x128 of one row takes the host 8.4 us
 # through Python's checks.)
 
 def _rng(rng, x: torch.Tensor, index: int):

@@ -6,8 +6,9 @@
 // outputs that are None, and calls the library on torch's current stream. It returns the
 // wrapper's result, or None where anything is not as the call wants it, or where the tensors'
 // GPU is not the current one: the wrapper then goes its own way, which raises the specific
-// error, or switches the device. Nothing is launched before every test has passed, and a status
-// other than DG_OK is a None too, so that the wrapper's own call reports it.
+// error, or switches the device. None means that the library has not been called. Once it has
+// been, its status is raised from here: a call may have run, in place too, whatever it reports,
+// and is never made a second time.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -16,6 +17,7 @@
 #include <c10/hip/HIPStream.h>
 
 #include <cstdint>
+#include <exception>
 
 #include "../../include/dg.h"
 
@@ -28,8 +30,9 @@ decltype(&dg_fp8_gemm_nt_gated_fp8) p_gated;
 decltype(&dg_gated_backward_fp8) p_gated_backward;
 decltype(&dg_dropout_add) p_dropout_add;
 decltype(&dg_dropout_backward_fp8) p_dropout_backward;
+PyObject* p_check;  // raises a status as the binding's exception
 
-struct NotPlain {};  // something is not as the call wants it
+struct NotPlain {};  // something is not as the call wants it; thrown before the library is called
 
 constexpr int64_t kBlock = 128;
 
@@ -148,31 +151,42 @@ void* stream_of(const at::Tensor& x) {
   return (void*)c10::hip::getCurrentHIPStream((c10::DeviceIndex)x.get_device()).stream();
 }
 
-// The library's call, without Python's lock: a launch may wait for room in its queue.
+// The library's call, without Python's lock: a launch may wait for room in its queue. An exception of
+// it becomes a status: thrown on, it would read as a call that was not made.
 template <class F, class... A>
 dg_status run(F f, A... a) {
   PyThreadState* state = PyEval_SaveThread();
-  const dg_status s = f(a...);
+  dg_status s = DG_ERR_LAUNCH;
+  try {
+    s = f(a...);
+  } catch (const std::exception&) {
+  }
   PyEval_RestoreThread(state);
   return s;
 }
 
+// The outputs of a call that was made, or nullptr with a Python exception set.
 template <class... O>
 PyObject* result(dg_status s, O&... out) {
-  if (s != DG_OK) throw NotPlain{};
+  if (s != DG_OK) {
+    PyObject* r = PyObject_CallFunction(p_check, "i", (int)s);
+    Py_XDECREF(r);
+    if (r) PyErr_Format(PyExc_RuntimeError, "status %d", (int)s);
+    return nullptr;
+  }
   if constexpr (sizeof...(O) == 1) return (Py_INCREF(out.o), ...), (out.o, ...);
   else return PyTuple_Pack(sizeof...(O), out.o...);
 }
 
-// f(args), with None for whatever f does not want and for every C++ exception.
+// f(args): its result or the exception it set, and None for whatever it threw before the
+// library's call.
 template <Py_ssize_t N, PyObject* (*F)(PyObject* const*)>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  PyObject* r = nullptr;
   try {
-    if (n == N) r = F(args);
-  } catch (...) {
+    if (n == N) return F(args);
+  } catch (const NotPlain&) {
+  } catch (const std::exception&) {  // no memory for an output
   }
-  if (r) return r;
   PyErr_Clear();
   Py_RETURN_NONE;
 }
@@ -293,10 +307,14 @@ PyObject* dropout_backward(PyObject* const* a) {
                 codes, sf, db);
 }
 
-// bind(addresses of the six calls, in the order of their declaration above)
+// bind(addresses of the six calls, in the order of their declaration above; check)
 PyObject* bind(PyObject*, PyObject* args) {
   unsigned long long f[6];
-  if (!PyArg_ParseTuple(args, "KKKKKK", f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+  PyObject* check;
+  if (!PyArg_ParseTuple(args, "KKKKKKO", f, f + 1, f + 2, f + 3, f + 4, f + 5, &check)) return nullptr;
+  Py_INCREF(check);
+  Py_XDECREF(p_check);
+  p_check = check;
   p_layernorm = (decltype(p_layernorm))f[0];
   p_layernorm_backward = (decltype(p_layernorm_backward))f[1];
   p_gated = (decltype(p_gated))f[2];
