@@ -70,11 +70,8 @@ dg_status launch_tile(const Problem& p0, int64_t blocks, hipStream_t stream) {
   const int64_t grid = blocks * p.tiles_m * p.tiles_n;
   if (grid <= 0) return DG_OK;
   if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "grid of %lld tiles", (long long)grid);
-  hipLaunchKernelGGL((gemm_kernel<Cfg, KIND>), dim3((unsigned)grid), dim3(Cfg::NT),
-                     Cfg::LDS_BYTES, stream, p);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
-  return DG_OK;
+  return launch_kernel("gemm_kernel", gemm_kernel<Cfg, KIND>, dim3((unsigned)grid), dim3(Cfg::NT),
+                       Cfg::LDS_BYTES, stream, p);
 }
 
 template <class Cfg, int KIND, int LAY, int EPI>
@@ -106,11 +103,8 @@ dg_status launch_pipe_as(const Problem& p0, int64_t blocks, const Epilogue& ep,
   }
   a.items = (int32_t)grid;
   const int64_t wgs = grid < kCUs ? grid : kCUs;  // persistent, one workgroup per CU
-  hipLaunchKernelGGL((pipe_kernel<Cfg, KIND, false, LAY, EPI>), dim3((unsigned)wgs), dim3(Cfg::NT),
-                     0, stream, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
-  return DG_OK;
+  return launch_kernel("pipe_kernel", pipe_kernel<Cfg, KIND, false, LAY, EPI>, dim3((unsigned)wgs),
+                       dim3(Cfg::NT), 0, stream, a);
 }
 
 template <class Cfg, int KIND, int LAY = 0>
@@ -148,11 +142,8 @@ dg_status launch_pipe_swiglu_as(const Problem& p0, int64_t blocks, int64_t I, ui
   a.sw.I = (int32_t)I;
   a.items = (int32_t)grid;
   const int64_t wgs = grid < kCUs ? grid : kCUs;  // persistent, one workgroup per CU
-  hipLaunchKernelGGL((pipe_kernel<Cfg, KIND, true>), dim3((unsigned)wgs), dim3(Cfg::NT), 0, stream,
-                     a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
-  return DG_OK;
+  return launch_kernel("pipe_kernel", pipe_kernel<Cfg, KIND, true>, dim3((unsigned)wgs),
+                       dim3(Cfg::NT), 0, stream, a);
 }
 
 template <int KIND>
@@ -311,10 +302,8 @@ dg_status launch_transpose(const uint8_t* src, uint8_t* dst, int64_t R, int64_t 
                            hipStream_t stream) {
   const int64_t tiles_c = (C + kTrTile - 1) / kTrTile, tiles = (R / kTrTile) * tiles_c;
   if (tiles > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED_SHAPE, "transpose of %lld tiles", (long long)tiles);
-  hipLaunchKernelGGL(transpose_bytes_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, src, dst,
-                     R, C, tiles_c);
-  const hipError_t err = hipGetLastError();
-  return err == hipSuccess ? DG_OK : fail(DG_ERR_LAUNCH, "transpose: %s", hipGetErrorString(err));
+  return launch_kernel("transpose_bytes_kernel", transpose_bytes_kernel, dim3((unsigned)tiles),
+                       dim3(256), 0, stream, src, dst, R, C, tiles_c);
 }
 
 // Most column tiles one XCD holds when groups of G consecutive tiles go to the XCDs
@@ -389,18 +378,9 @@ dg_status launch_skinny(const Problem& p0, int64_t blocks, hipStream_t stream) {
     dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
     if (st != DG_OK) return st;
   }
-  if (LAY != 0)
-    hipLaunchKernelGGL((skinny_kernel<Cfg, false, LAY>), dim3((unsigned)grid), dim3(Cfg::NT),
-                       lds_bytes, stream, a);
-  else if (p0.sfa_packed)
-    hipLaunchKernelGGL((skinny_kernel<Cfg, true>), dim3((unsigned)grid), dim3(Cfg::NT),
-                       lds_bytes, stream, a);
-  else
-    hipLaunchKernelGGL((skinny_kernel<Cfg, false>), dim3((unsigned)grid), dim3(Cfg::NT),
-                       lds_bytes, stream, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
-  return DG_OK;
+  const auto kernel = LAY != 0 ? skinny_kernel<Cfg, false, LAY>
+                      : p0.sfa_packed ? skinny_kernel<Cfg, true> : skinny_kernel<Cfg, false>;
+  return launch_kernel("skinny_kernel", kernel, dim3((unsigned)grid), dim3(Cfg::NT), lds_bytes, stream, a);
 }
 
 // ---------------------------------------------------------------- stream kernel
@@ -453,15 +433,9 @@ dg_status launch_stream(const Problem& p0, int64_t blocks, hipStream_t stream) {
     dg_status st = get_workspace(stream, part, (size_t)pl.tiles, &a.ws, &a.counters);
     if (st != DG_OK) return st;
   }
-  if (LAY != 0)
-    hipLaunchKernelGGL((stream_kernel<Cfg, false, LAY>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
-  else if (p0.sfa_packed)
-    hipLaunchKernelGGL((stream_kernel<Cfg, true>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
-  else
-    hipLaunchKernelGGL((stream_kernel<Cfg, false>), dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
-  return DG_OK;
+  const auto kernel = LAY != 0 ? stream_kernel<Cfg, false, LAY>
+                      : p0.sfa_packed ? stream_kernel<Cfg, true> : stream_kernel<Cfg, false>;
+  return launch_kernel("stream_kernel", kernel, dim3((unsigned)pl.grid), dim3(Cfg::NT), 0, stream, a);
 }
 
 // ---------------------------------------------------------------- ring kernel
@@ -536,10 +510,7 @@ dg_status launch_ring_as(const Problem& p, const Epilogue& ep, hipStream_t strea
     const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
     if (st != DG_OK) return st;
   }
-  hipLaunchKernelGGL((ring_kernel<Cfg, EPI>), dim3((unsigned)grid), dim3(Cfg::NT), 0, stream, a);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "launch: %s", hipGetErrorString(err));
-  return DG_OK;
+  return launch_kernel("ring_kernel", ring_kernel<Cfg, EPI>, dim3((unsigned)grid), dim3(Cfg::NT), 0, stream, a);
 }
 
 // The forms by rows and sfA layout. kRing64, kRing128: tiles of 64 or 128 columns and up to 64
@@ -1210,15 +1181,9 @@ dg_status dg_quantize_fp8_1x128(const void* x, int32_t x_dtype, void* codes, flo
   const int64_t per_wg = (int64_t)(kQuantThreads / 64) * kQuantBlocksPerWave * kQuantUnroll;
   int64_t grid = (nblocks + per_wg - 1) / per_wg;
   if (grid > 8 * kCUs) grid = 8 * kCUs;  // grid-stride beyond eight workgroups per CU
-  if (x_dtype == DG_DTYPE_BF16)
-    hipLaunchKernelGGL(quant_kernel<true>, dim3((unsigned)grid), dim3(kQuantThreads), 0,
-                       (hipStream_t)stream, x, (uint8_t*)codes, sf, nblocks);
-  else
-    hipLaunchKernelGGL(quant_kernel<false>, dim3((unsigned)grid), dim3(kQuantThreads), 0,
-                       (hipStream_t)stream, x, (uint8_t*)codes, sf, nblocks);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(DG_ERR_LAUNCH, "quant_kernel: %s", hipGetErrorString(err));
-  return DG_OK;
+  return launch_kernel("quant_kernel", x_dtype == DG_DTYPE_BF16 ? quant_kernel<true> : quant_kernel<false>,
+                       dim3((unsigned)grid), dim3(kQuantThreads), 0, (hipStream_t)stream, x,
+                       (uint8_t*)codes, sf, nblocks);
 }
 
 int32_t dg_num_configs(void) { return kNumCfg; }
@@ -1301,11 +1266,6 @@ dg_status check_norm(int32_t x_dtype, int32_t w_dtype, int64_t M, int64_t K) {
   return DG_OK;
 }
 
-dg_status launched(const char* what) {
-  const hipError_t err = hipGetLastError();
-  return err == hipSuccess ? DG_OK : fail(DG_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(err));
-}
-
 // The stream's workspace as `count` partial sums.
 dg_status get_partials(hipStream_t st, int64_t count, float** part) {
   return no_throw([&] {
@@ -1320,9 +1280,9 @@ dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N,
   constexpr int64_t kMost = (int64_t)1 << 28;
   for (int64_t n = 0; n < N; n += kMost) {
     const int64_t cols = N - n < kMost ? N - n : kMost;
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, st,
-                       R > 0 ? part + n : part, out + n, (int)R, (int)N, nullptr, (int)cols);
-    const dg_status s = launched("column_sum_kernel");
+    const dg_status s = launch_kernel("column_sum_kernel", column_sum_kernel, dim3((unsigned)(cols / 32)),
+                                      dim3(256), 0, st, R > 0 ? part + n : part, out + n, (int)R, (int)N,
+                                      nullptr, (int)cols);
     if (s != DG_OK) return s;
   }
   return DG_OK;
@@ -1331,9 +1291,8 @@ dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N,
 // The same for part[R][2 N], whose halves go to out and out2 (NULL: not wanted). N <= 2^27.
 dg_status launch_column_sum2(const float* part, float* out, float* out2, int64_t R, int64_t N,
                              hipStream_t st) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((out2 ? 2 : 1) * N / 32)), dim3(256), 0, st, part,
-                     out, (int)R, (int)(2 * N), out2, (int)N);
-  return launched("column_sum_kernel");
+  return launch_kernel("column_sum_kernel", column_sum_kernel, dim3((unsigned)((out2 ? 2 : 1) * N / 32)),
+                       dim3(256), 0, st, part, out, (int)R, (int)(2 * N), out2, (int)N);
 }
 
 }  // namespace dg
@@ -1379,7 +1338,7 @@ dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dt
                                void* codes, void* sf, int32_t sf_packed, int64_t M, int64_t K,
                                void* stream) {
   g_detail[0] = 0;
-  const dg_status s = check_norm(x_dtype, w_dtype, M, K);
+  dg_status s = check_norm(x_dtype, w_dtype, M, K);
   if (s != DG_OK) return s;
   if (!(eps > 0.f && eps < INFINITY)) return fail(DG_ERR_BAD_SHAPE, "eps=%g is not positive", (double)eps);
   if (M == 0 || K == 0) return DG_OK;
@@ -1400,10 +1359,10 @@ dg_status dg_rmsnorm_fp8_1x128(const void* x, const void* residual, int32_t x_dt
     // fp32 with four chunks spills 62 or 86 of them all the same (1000 x 24576, three chunks,
     // 59.1 us, 5.4 TB/s; 1000 x 32768 124, 3.4)
     constexpr bool ahead = c.value <= (xb.value ? 3 : 2);
-    hipLaunchKernelGGL((rmsnorm_kernel<xb.value, wb.value, c.value, ahead>), grid, block, 0,
-                       (hipStream_t)stream, a);
+    s = launch_kernel("rmsnorm_kernel", rmsnorm_kernel<xb.value, wb.value, c.value, ahead>, grid, block, 0,
+                      (hipStream_t)stream, a);
   });
-  return launched("rmsnorm_kernel");
+  return s;
 }
 
 dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
@@ -1441,10 +1400,9 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* dh, const void* h, int
     // what 256 registers hold, or nearly: fp32 with two chunks ahead spills 6 or 7 of them, three
     // not ahead 2 or 8, four 82 or 86 (1000 x 24576 84.5 us, 4.65 TB/s; 1000 x 32768 165, 3.2)
     constexpr bool ahead = c.value <= 2;
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<xb.value, wb.value, c.value, ahead>), dim3(grid),
-                       dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
+    s = launch_kernel("rmsnorm_backward_kernel", rmsnorm_backward_kernel<xb.value, wb.value, c.value, ahead>,
+                      dim3(grid), dim3((unsigned)(nt * R)), (size_t)((R - 1) * K) * sizeof(float), st, a);
   });
-  s = launched("rmsnorm_backward_kernel");
   return s == DG_OK && !direct ? launch_column_sum(part, dweight, G, K, st) : s;
 }
 
@@ -1475,8 +1433,7 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
                ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(N / 128)}, part, dbias, M, pl.rows,
                (int32_t)N, activation, (int32_t)pl.strips, (int32_t)pl.groups};
   const unsigned grid = (unsigned)(pl.strips * pl.groups + (direct ? N / 64 : 0));
-  hipLaunchKernelGGL(act_backward_kernel, dim3(grid), dim3(256), 0, st, a);
-  s = launched("act_backward_kernel");
+  s = launch_kernel("act_backward_kernel", act_backward_kernel, dim3(grid), dim3(256), 0, st, a);
   return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, N, st) : s;
 }
 

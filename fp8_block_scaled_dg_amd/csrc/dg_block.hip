@@ -79,8 +79,7 @@ dg_status launch_layernorm_backward(const LayerNormBwdArgs& a, unsigned grid, un
   size_t bytes = (size_t)(lds_dw ? a.K : (a.teams - 1) * a.K) * sizeof(float);
   const size_t direct = (size_t)threads * 2 * Pieces<BF16>::P * sizeof(float);
   if (!a.part && direct > bytes) bytes = direct;
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), bytes, st, a);
-  return DG_OK;
+  return launch_kernel("layernorm_backward_kernel", kernel, dim3(grid), dim3(threads), bytes, st, a);
 }
 
 // ---------------------------------------------------------------- gated product
@@ -109,9 +108,8 @@ dg_status launch_pipe_gated(const Problem& p0, const Epilogue& ep, hipStream_t s
   }
   a.items = (int32_t)grid;
   const int64_t wgs = grid < kCUs ? grid : kCUs;  // persistent, one workgroup per CU
-  hipLaunchKernelGGL((pipe_kernel<Cfg, kDense, false, 0, kEpiGated>), dim3((unsigned)wgs), dim3(Cfg::NT),
-                     0, stream, a);
-  return launched("pipe_kernel");
+  return launch_kernel("pipe_kernel", pipe_kernel<Cfg, kDense, false, 0, kEpiGated>, dim3((unsigned)wgs),
+                       dim3(Cfg::NT), 0, stream, a);
 }
 
 constexpr int64_t kLaunchThreads = (int64_t)1 << 32;  // a launch holds fewer
@@ -134,8 +132,8 @@ dg_status launch_gated_ring_as(const Problem& p, int64_t S, const Epilogue& ep, 
     const dg_status st = get_workspace(stream, part, (size_t)tiles, &a.ws, &a.counters);
     if (st != DG_OK) return st;
   }
-  hipLaunchKernelGGL(gated_ring_kernel<Cfg>, dim3((unsigned)grid), dim3(Cfg::NT), 0, stream, a);
-  return launched("gated_ring_kernel");
+  return launch_kernel("gated_ring_kernel", gated_ring_kernel<Cfg>, dim3((unsigned)grid), dim3(Cfg::NT), 0,
+                       stream, a);
 }
 
 template <bool PACKED, bool STREAM_B>
@@ -252,11 +250,9 @@ dg_status dg_dropout_add(const void* x, const void* residual, int32_t x_dtype, d
     return fail(DG_ERR_MISALIGNED, "x, residual and out must be 16-byte aligned");
   const int64_t per_wg = kDropChunk * (kDropThreads / 64) * kDropUnroll;
   const dim3 grid((unsigned)even_grid((n + per_wg - 1) / per_wg, 8 * kCUs)), block(kDropThreads);
-  if (x_dtype == DG_DTYPE_BF16)
-    hipLaunchKernelGGL(dropout_add_kernel<true>, grid, block, 0, (hipStream_t)stream, a);
-  else
-    hipLaunchKernelGGL(dropout_add_kernel<false>, grid, block, 0, (hipStream_t)stream, a);
-  return launched("dropout_add_kernel");
+  return launch_kernel("dropout_add_kernel",
+                       x_dtype == DG_DTYPE_BF16 ? dropout_add_kernel<true> : dropout_add_kernel<false>, grid,
+                       block, 0, (hipStream_t)stream, a);
 }
 
 dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropout_p,
@@ -289,11 +285,9 @@ dg_status dg_dropout_backward_fp8(const void* dy, int32_t dy_dtype, double dropo
   const DropBwdArgs a{dy, (uint8_t*)codes, ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(K / 128)}, part,
                       dbias, M, pl.rows, (int32_t)K, (int32_t)pl.strips, (int32_t)pl.groups, drop};
   const dim3 grid((unsigned)(pl.strips * pl.groups + (direct ? K / kDropDirectCols : 0)));
-  if (dy_dtype == DG_DTYPE_BF16)
-    hipLaunchKernelGGL(dropout_backward_kernel<true>, grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(dropout_backward_kernel<false>, grid, dim3(256), 0, st, a);
-  s = launched("dropout_backward_kernel");
+  s = launch_kernel("dropout_backward_kernel",
+                    dy_dtype == DG_DTYPE_BF16 ? dropout_backward_kernel<true> : dropout_backward_kernel<false>,
+                    grid, dim3(256), 0, st, a);
   return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, K, st) : s;
 }
 
@@ -320,14 +314,12 @@ dg_status dg_layernorm_fp8_1x128(const void* x, const void* residual, int32_t x_
   const int resident = norm_chunks(K) == 1 ? 1024 / nt : 1;  // as for the RMS norm
   const dim3 grid((unsigned)even_grid(M, kCUs * resident)), block((unsigned)nt);
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
-    if (a.drop.threshold)
-      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, true>), grid, block, 0,
-                         (hipStream_t)stream, a);
-    else
-      hipLaunchKernelGGL((layernorm_kernel<xb.value, wb.value, c.value, false>), grid, block, 0,
-                         (hipStream_t)stream, a);
+    s = launch_kernel("layernorm_kernel",
+                      a.drop.threshold ? layernorm_kernel<xb.value, wb.value, c.value, true>
+                                       : layernorm_kernel<xb.value, wb.value, c.value, false>,
+                      grid, block, 0, (hipStream_t)stream, a);
   });
-  return launched("layernorm_kernel");
+  return s;
 }
 
 dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, int32_t x_dtype,
@@ -365,8 +357,6 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
   norm_form(x_dtype == DG_DTYPE_BF16, w_dtype == DG_DTYPE_BF16, K, [&](auto xb, auto wb, auto c) {
     s = launch_layernorm_backward<xb.value, wb.value, c.value>(a, grid, (unsigned)(nt * R), st);
   });
-  if (s != DG_OK) return s;
-  s = launched("layernorm_backward_kernel");
   return s == DG_OK && !direct ? launch_column_sum2(part, dweight, dbias, G, K, st) : s;
 }
 
@@ -436,9 +426,9 @@ dg_status dg_gated_backward_fp8(const void* dh, const void* pre, int32_t activat
   const GatedBwdArgs a{(const uint16_t*)dh, (const uint16_t*)pre, (uint8_t*)codes,
                        ScaleOut{(uint8_t*)sf, sf_packed != 0, (int32_t)(I / 64)}, part, dbias, M, pl.rows,
                        (int32_t)I, activation, (int32_t)pl.strips, (int32_t)pl.groups};
-  hipLaunchKernelGGL(gated_backward_kernel, dim3((unsigned)(pl.strips * pl.groups + (direct ? I / kGatedDirectCols : 0))),
-                     dim3(256), 0, st, a);
-  s = launched("gated_backward_kernel");
+  s = launch_kernel("gated_backward_kernel", gated_backward_kernel,
+                    dim3((unsigned)(pl.strips * pl.groups + (direct ? I / kGatedDirectCols : 0))), dim3(256), 0, st,
+                    a);
   return s == DG_OK && sum ? launch_column_sum(part, dbias, pl.groups, 2 * I, st) : s;
 }
 

@@ -7,7 +7,9 @@
 #include <cstdint>
 #include <exception>
 #include <mutex>
+#include <tuple>
 #include <type_traits>
+#include <utility>
 
 #include "../../include/dg.h"
 #include "gemm_kernel.hpp"
@@ -26,7 +28,6 @@ dg_status check_common(const void* A, const void* B, const void* C, const void* 
 dg_status check_rows(int64_t M, int64_t K, const char* k);
 void print_dense_choice(int64_t M, int64_t N, int64_t K, const char* config, const char* note);
 dg_status check_norm(int32_t x_dtype, int32_t w_dtype, int64_t M, int64_t K);
-dg_status launched(const char* what);
 dg_status get_partials(hipStream_t st, int64_t count, float** part);
 dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N, hipStream_t st);
 dg_status launch_column_sum2(const float* part, float* out, float* out2, int64_t R, int64_t N,
@@ -71,6 +72,23 @@ dg_status no_throw(F f) noexcept {
   } catch (...) {
     return fail(DG_ERR_LAUNCH, "host code: an unknown exception");
   }
+}
+
+// Launches kernel(args...) and reports what this launch returned. hipGetLastError would also report
+// an error that some earlier call left in the thread, of a launch that then runs all the same.
+template <class... P, class... A>
+dg_status launch_kernel(const char* what, void (*kernel)(P...), dim3 grid, dim3 block, size_t lds,
+                        hipStream_t stream, A&&... args) {
+  std::tuple<P...> values(std::forward<A>(args)...);
+  const hipError_t e = std::apply(
+      [&](P&... v) {
+        void* ptrs[] = {(void*)&v...};
+        return hipLaunchKernel((const void*)kernel, grid, block, ptrs, lds, stream);
+      },
+      values);
+  if (e == hipSuccess) return DG_OK;
+  (void)hipGetLastError();  // reported here, and not again by whoever asks next
+  return fail(DG_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
 }
 
 // The pipelined kernel addresses a tile's rows with 32-bit offsets below 256 * K
