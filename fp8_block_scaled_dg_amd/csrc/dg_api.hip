@@ -63,7 +63,7 @@ dg_status launch_tile(const Problem& p0, int64_t blocks, hipStream_t stream) {
                                    hipFuncAttributeMaxDynamicSharedMemorySize, Cfg::LDS_BYTES);
   });
   if (attr_err != hipSuccess)
-    return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(attr_err));
+    return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", take_error(attr_err));
   Problem p = p0;
   p.tiles_m = (int32_t)((p.M + Cfg::BM - 1) / Cfg::BM);
   p.tiles_n = (int32_t)((p.N + Cfg::BN - 1) / Cfg::BN);
@@ -188,7 +188,7 @@ dg_status grow(Workspace& w, void** buf, size_t* have, size_t need, size_t elem,
   hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
   hipError_t e = hipStreamIsCapturing(stream, &cap);
   if (e != hipSuccess)
-    return fail(DG_ERR_LAUNCH, "hipStreamIsCapturing: %s", hipGetErrorString(e));
+    return fail(DG_ERR_LAUNCH, "hipStreamIsCapturing: %s", take_error(e));
   if (cap != hipStreamCaptureStatusNone)
     return fail(DG_ERR_CAPTURE,
                 "the stream is being captured and this shape needs a larger library "
@@ -197,12 +197,12 @@ dg_status grow(Workspace& w, void** buf, size_t* have, size_t need, size_t elem,
   void* fresh = nullptr;
   e = hipMalloc(&fresh, need * elem);
   if (e != hipSuccess)
-    return fail(DG_ERR_LAUNCH, "workspace hipMalloc(%zu): %s", need * elem, hipGetErrorString(e));
+    return fail(DG_ERR_LAUNCH, "workspace hipMalloc(%zu): %s", need * elem, take_error(e));
   if (zero) {
     e = hipMemsetAsync(fresh, 0, need * elem, stream);
     if (e != hipSuccess) {
       (void)hipFree(fresh);
-      return fail(DG_ERR_LAUNCH, "workspace clear: %s", hipGetErrorString(e));
+      return fail(DG_ERR_LAUNCH, "workspace clear: %s", take_error(e));
     }
   }
   if (*buf) w.retired.push_back(*buf);
@@ -244,14 +244,14 @@ dg_status scratch_workspace(size_t partial_bytes, size_t counters, float** parti
                 partial_bytes, counters, kScratchPartialBytes, kScratchCounters);
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", take_error(e));
   std::lock_guard<std::mutex> lock(g_scratch_mu);
   auto it = g_scratch_ptr.find(dev);
   if (it == g_scratch_ptr.end()) {
     uint8_t* ptr = nullptr;
     e = hipGetSymbolAddress((void**)&ptr, HIP_SYMBOL(scratch));
     if (e != hipSuccess || !ptr)
-      return fail(DG_ERR_LAUNCH, "hipGetSymbolAddress(scratch): %s", hipGetErrorString(e));
+      return fail(DG_ERR_LAUNCH, "hipGetSymbolAddress(scratch): %s", take_error(e));
     it = g_scratch_ptr.emplace(dev, ptr).first;
   }
   *partials = (float*)it->second;
@@ -266,7 +266,7 @@ dg_status get_workspace(hipStream_t stream, size_t partial_bytes, size_t counter
   if (g_noalloc) return scratch_workspace(partial_bytes, counters, partials, counter_ptr);
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", take_error(e));
   std::lock_guard<std::mutex> lock(g_ws_mu);
   Workspace& w = g_ws[std::make_pair(dev, stream)];
   dg_status st = grow(w, &w.partials, &w.partial_bytes, partial_bytes, 1, stream, false);
@@ -285,7 +285,7 @@ dg_status get_transpose_workspace(hipStream_t stream, size_t a_bytes, size_t b_b
                                   uint8_t** a, uint8_t** b) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", take_error(e));
   std::lock_guard<std::mutex> lock(g_ws_mu);
   Workspace& w = g_ws[std::make_pair(dev, stream)];
   dg_status st = grow(w, &w.a_t, &w.a_t_bytes, a_bytes, 1, stream, false);
@@ -348,7 +348,7 @@ dg_status launch_skinny(const Problem& p0, int64_t blocks, hipStream_t stream) {
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
   });
   if (attr_err != hipSuccess)
-    return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(attr_err));
+    return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", take_error(attr_err));
   SkinnyArgs a{};
   a.p = p0;
   const int KB = (int)(p0.K / kKBlock);
@@ -823,14 +823,14 @@ dg_status dg_release_workspaces(void) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
   int cur = 0;
   hipError_t e = hipGetDevice(&cur);
-  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", take_error(e));
   std::set<int> devs;
   for (auto& kv : g_ws) devs.insert(kv.first.first);
   // nothing may still run on the buffers: wait for every device that holds some
   for (int d : devs) {
     if ((e = hipSetDevice(d)) != hipSuccess || (e = hipDeviceSynchronize()) != hipSuccess) {
       (void)hipSetDevice(cur);
-      return fail(DG_ERR_LAUNCH, "synchronizing device %d: %s", d, hipGetErrorString(e));
+      return fail(DG_ERR_LAUNCH, "synchronizing device %d: %s", d, take_error(e));
     }
   }
   for (auto& kv : g_ws) {

@@ -74,7 +74,7 @@ dg_status launch_layernorm_backward(const LayerNormBwdArgs& a, unsigned grid, un
                               kNormMaxK * (int)sizeof(float));
       if (e == hipSuccess && dev <= 63) done.fetch_or(bit);
     }
-    if (e != hipSuccess) return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", hipGetErrorString(e));
+    if (e != hipSuccess) return fail(DG_ERR_LAUNCH, "hipFuncSetAttribute: %s", take_error(e));
   }
   size_t bytes = (size_t)(lds_dw ? a.K : (a.teams - 1) * a.K) * sizeof(float);
   const size_t direct = (size_t)threads * 2 * Pieces<BF16>::P * sizeof(float);

@@ -33,6 +33,13 @@ dg_status launch_column_sum(const float* part, float* out, int64_t R, int64_t N,
 dg_status launch_column_sum2(const float* part, float* out, float* out2, int64_t R, int64_t N,
                              hipStream_t st);
 
+// The text of a failed runtime call's error. HIP keeps the error for whoever asks the thread for its
+// last one; it is reported here, so it is taken off, and no later call of anyone is blamed for it.
+inline const char* take_error(hipError_t e) {
+  (void)hipGetLastError();
+  return hipGetErrorString(e);
+}
+
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 inline bool known_dtype(int32_t t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
@@ -86,9 +93,7 @@ dg_status launch_kernel(const char* what, void (*kernel)(P...), dim3 grid, dim3 
         return hipLaunchKernel((const void*)kernel, grid, block, ptrs, lds, stream);
       },
       values);
-  if (e == hipSuccess) return DG_OK;
-  (void)hipGetLastError();  // reported here, and not again by whoever asks next
-  return fail(DG_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
+  return e == hipSuccess ? DG_OK : fail(DG_ERR_LAUNCH, "%s: %s", what, take_error(e));
 }
 
 // The pipelined kernel addresses a tile's rows with 32-bit offsets below 256 * K
