@@ -188,7 +188,8 @@ double gated_pipe_time(int64_t M, int64_t I, int64_t K) {
          11.3 * filled;
 }
 
-// The tile kernel's 32-bit offsets reach from a gate row to its up row.
+// The tile kernel's 32-bit offsets reach from a gate row to its up row. Beyond that only the ring
+// kernel is left, whose launches hold fewer than 2^23 workgroups of 512 threads.
 bool gated_pipe_fits(int64_t I, int64_t K) { return (I + 256) * K < (int64_t)1 << 31; }
 
 GatedPlan gated_plan(int64_t M, int64_t I, int64_t K) {
@@ -214,6 +215,10 @@ constexpr int64_t kGatedStreamB = int64_t(96) << 20;
 dg_status gated(const Problem& p, const Epilogue& ep, hipStream_t stream) {
   const int64_t I = p.N / 2;
   const GatedPlan pl = gated_plan(p.M, I, p.K);
+  if (pl.bm == 0 && !gated_pipe_fits(I, p.K))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE,
+                "(I + 256) * K beyond 2^31 with 2^23 tiles of 64 x 128 or more (M=%lld, I=%lld, K=%lld)",
+                (long long)p.M, (long long)I, (long long)p.K);
   if (pl.bm == 0) {
     print_dense_choice(p.M, p.N, p.K, "pipe128x256", " (gated)");
     return p.K / kKBlock >= kLongKB ? launch_pipe_gated<PipeCfg<128, 256, 12>>(p, ep, stream)

@@ -452,9 +452,10 @@ dg_status dg_layernorm_backward(const void* dy, const void* dh, const void* h, i
  *   sfB   fp32 [2 I / 128][K/128];  bias [2 I] fp32 or bf16 (bias_dtype), NULL: none
  *   codes e4m3fn [M][I];  sf fp32 [M][I/128] or (sf_packed) uint32 [M][ceil(I/512)]
  *   pre   bf16 [M][2 I] = z, for dg_gated_backward_fp8; NULL: not stored
- * I % 128 == 0, I <= 2^29, M <= 2^30, K <= 2^22, I * K < 2^42; alignment, stream, workspace and error rules of
- * dg_fp8_gemm_nt_bias_act_fp8. Codes and scales of a block holding an infinity or NaN are
- * unspecified.
+ * I % 128 == 0, I <= 2^29, M <= 2^30, K <= 2^22, I * K < 2^42, and where (I + 256) * K >= 2^31
+ * ceil(M / 64) * I / 128 < 2^23 (DG_ERR_UNSUPPORTED_SHAPE beyond); alignment, stream, workspace
+ * and error rules of dg_fp8_gemm_nt_bias_act_fp8. Codes and scales of a block holding an infinity
+ * or NaN are unspecified.
  */
 dg_status dg_fp8_gemm_nt_gated_fp8(const void* A, const void* B, void* codes, void* sf,
                                    int32_t sf_packed, const void* sfA, int32_t sfA_packed,
