@@ -11,9 +11,10 @@ gate and up projections (one product of the stacked weights [Wg; Wu], whose epil
 biases, gates and writes W2's FP8 operand), then W2's product with its bias. Backward, five calls: dropout's
 gradient as W2's FP8 operand with b2's gradient, the product by W2, the gate's backward with its bias
 gradients, the product by [Wg; Wu], the layer norm's backward, which adds the residual stream's
-gradient. Masks are drawn again from rng = (seed, offset) on the GPU, so a captured step draws new
-ones when the offset is counted up between replays. The projections stay frozen: their gradients
-contract over tokens, along which the FP8 gradients have no scale blocks.
+gradient. Masks are drawn again from rng = (seed, offset) on the GPU; the L + 1 places that drop use
+subsequences 0 .. L, and a mask depends on offset + subsequence, so that advance() counts the offset
+up by L + 1 after a step (captured with it, each replay draws new masks). The projections stay
+frozen: their gradients contract over tokens, along which the FP8 gradients have no scale blocks.
 
     python examples/prenorm_gated.py [--tokens 4096] [--hidden 2048] [--ffn 7168] [--layers 2]
                                      [--activation silu] [--dropout 0.1]
@@ -50,6 +51,10 @@ class PreNormGated:
         self.layers = [Layer(hidden, ffn, lambda *shape: torch.randn(shape, generator=gen, device=device))
                        for _ in range(layers)]
         self.rng = torch.tensor([seed, 0], dtype=torch.int64, device=device)
+
+    def advance(self):
+        """The next step's masks: none of them is one of this step's."""
+        self.rng[1].add_(len(self.layers) + 1)
 
     def forward(self, x, train=True):
         """x bf16 [tokens, hidden] -> (result, what backward needs)."""
@@ -129,6 +134,7 @@ def main():
     x, dout = (torch.randn(a.tokens, a.hidden, device="cuda").to(BF) for _ in range(2))
     for name, d in compare(model, x, dout).items():
         print(f"{name:9s} {d:.4f} from fp32 torch")
+    model.advance()
     saved = model.forward(x)[1]
     flops = 6 * a.tokens * a.hidden * a.ffn * a.layers
     for name, f in (("forward", lambda: model.forward(x)), ("inference", lambda: model.forward(x, train=False)),

@@ -707,10 +707,12 @@ def dropout_add(x, p, rng, subsequence=0, residual=None, out=None):
     """dropout(x) + residual (float32 or bfloat16 of any shape; residual optional), rounded once.
     An element is dropped with probability p (to the nearest 2^-16) and otherwise divided by
     1 - p. The mask depends on the element's index, rng's values (int64 [2] on the GPU: seed,
-    offset; read when the kernel runs) and subsequence, which is added to the offset: a training
-    loop counts the offset up, in a captured graph too, and gives each layer its subsequence. No
-    mask is stored: backward calls name the same values. Returns out, which may be x or residual
-    itself. Without a residual this is dropout's own gradient too."""
+    offset; read when the kernel runs) and subsequence, which is added to the offset: only the
+    sum counts. A training loop gives each of its n places a subsequence 0 .. n - 1 and counts
+    the offset up by n or more for each step, in a captured graph too; by less, a place would
+    repeat a mask that another one had the step before. No mask is stored: backward calls name
+    the same values. Returns out, which may be x or residual itself. Without a residual this is
+    dropout's own gradient too."""
     done = _marshal.dropout_add(x, p, rng, subsequence, residual, out)
     if done is not None:
         return done

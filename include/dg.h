@@ -373,8 +373,11 @@ dg_status dg_bias_act_backward_fp8(const void* dc, const void* pre, int32_t acti
  * and the two words of offset + subsequence (64 bits, wrapping).
  *   rng  int64 [2] in device memory: seed, offset, read when the kernel runs, so that a
  *        captured graph draws new masks when the caller changes them between replays
- * Calls with the same rng values, subsequence and shape draw the same mask (the backward of a
- * call names its values again); other offsets or subsequences draw independent ones.
+ * Only the sum offset + subsequence counts: calls with the same seed, the same sum and the same
+ * shape draw the same mask (the backward of a call names its values again), with another sum an
+ * independent one. Where a step uses subsequences 0 .. n - 1, the next step's offset therefore has
+ * to be at least n further on; counted up by one, place i would repeat the mask that place i + 1
+ * had the step before.
  * 0 <= p, and p rounds to less than one in 2^-16 steps; with p = 0 rng may be NULL. A dropped
  * NaN or infinity is 0.
  */
