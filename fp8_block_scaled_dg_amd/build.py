@@ -67,6 +67,19 @@ def _compile(cmd: list[str], what: str, verbose: bool) -> None:
         sys.stderr.write("\n".join(msgs) + "\n")
 
 
+def build_marshal(verbose: bool = False) -> bool:
+    """_marshal.so, which only saves host time: libdg.so needs hipcc alone, so where g++, torch's or
+    Python's headers are missing the build goes on and the binding checks arguments in Python."""
+    try:
+        _compile(marshal_command(), "_marshal.so", verbose)
+        return True
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(MARSHAL_PATH):
+            os.remove(MARSHAL_PATH)  # of other sources
+        sys.stderr.write(f"_marshal.so is not built ({e}): the binding checks arguments in Python\n")
+        return False
+
+
 def build(verbose: bool = False, out: str = LIB_PATH, extra: list[str] | None = None) -> str:
     """Compiles the translation units of libdg.so, the binding's marshalling module and the probe
     library side by side, then links libdg.so."""
@@ -75,12 +88,13 @@ def build(verbose: bool = False, out: str = LIB_PATH, extra: list[str] | None = 
         units = [(src, os.path.join(tmp, os.path.basename(src) + ".o")) for src in SOURCES]
         jobs = [(["hipcc", *compile_only, f'-DDG_BUILD_ID="{source_hash()}"', *(extra or []), "-c", "-o", obj,
                   src], os.path.basename(src)) for src, obj in units]
-        jobs.append((marshal_command(), "_marshal.so"))
         jobs.append((["hipcc", *HIPCC_FLAGS, "-o", PROBE_LIB_PATH, *PROBE_SOURCES], "libdg_probe.so"))
-        with ThreadPoolExecutor(len(jobs)) as pool:
+        with ThreadPoolExecutor(len(jobs) + 1) as pool:
+            marshal = pool.submit(build_marshal, verbose)
             list(pool.map(lambda job: _compile(*job, verbose), jobs))
+            marshal.result()
         _compile(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", out, *(obj for _, obj in units)],
-               "libdg.so", verbose)
+                 "libdg.so", verbose)
     return out
 
 
