@@ -143,19 +143,22 @@ dg_status launch_gated_ring(int bm, int64_t S, const Problem& p, const Epilogue&
   return launch_gated_ring_as<GatedCfg<2, 2, 2, PACKED, STREAM_B>>(p, S, ep, st);
 }
 
-// Estimated times in us, fitted to measurements on one MI355X: 530 products of 1 to 2048 rows, 256
-// to 18432 columns of h, K = 512 to 18432, the kernels' every form that fits (bm rows, S splits),
-// most of them with so many weights in turn that each came from HBM. On them the choice is within
-// 1.1 % of the best form measured on average, within 10 % on all but 16 (the worst, 1500 x 256 x
-// 2048: 15 - 29 %).
+// Estimated times in us, fitted to measurements on one MI355X: products of 1 to 2048 rows, 256 to
+// 18432 columns of h, K = 512 to 18432, the kernels' every form that fits (bm rows, S splits). On
+// 227 of them with so many weights in turn that each came from HBM the choice is within 0.6 % of the
+// best form measured on average and within 10 % on all; on 86 with three weights in turn within 1.9 %,
+// and within 10 % on all but three (32 x 14336 x 2048, 32 x 1024 x 1408, 96 x 18432 x 512: 17 - 18 %).
 //   ring: launch, prologue and epilogue; the run's pairs; B's bytes; further rounds of tiles; for
 //   S > 1 the partials' trip through memory and the last split's sum over them.
-//   us by S:            1     2     3     4     6     8    14
-//    M = 1,  I = 2048, K = 7168, bm = 16   38.1  23.4  19.0  15.7  13.8  13.1  13.7  (tiles 25.6)
-//    M = 64, I = 2048, K = 7168, bm = 64   46.6  29.5  24.8  21.2  19.8  20.3  23.9  (28.3)
-//    M = 64, I = 8192, K = 8192, bm = 64   55.3  40.6  32.2  31.9                    (62.9)
-//    M = 1000, I = 2048, K = 7168          44.0 - 45.8 (bm = 32: 76)                 (46.6 - 47.5)
-//    M = 2048, I = 2816, K = 4096          76.9                                      (70.3)
+// us by S, weights from HBM, the form taken in brackets:
+//                                              1     2     3     4     5     6     7    10    14  (tiles)
+//    M = 1,  I = 2048, K = 7168, bm = 16     37.9  23.3  18.9  15.5  14.7  13.7 [12.8] 13.1  13.6   25.4
+//    M = 16, I = 2048, K = 7168, bm = 16     39.4  24.4  19.7  16.3  15.4  14.4 [13.6] 13.6  14.0   26.9
+//    M = 64, I = 2048, K = 7168, bm = 32     40.2  25.2  20.8  17.3  17.0  16.1 [15.6]              28.2
+//                                bm = 64     46.3  29.4  24.6  21.2  21.0  19.8  19.5  21.4  23.8
+//    M = 64, I = 8192, K = 8192, bm = 64     55.2  40.6  32.2 [31.7]                                48.4
+//    M = 1000, I = 2048, K = 7168, bm = 64  [43.9]                                                  46.3
+//    M = 2048, I = 2816, K = 4096, bm = 64   76.0                                                  [67.3]
 struct GatedPlan {
   int bm;  // 0: the tile kernel
   int64_t S;
@@ -171,8 +174,10 @@ GatedPlan gated_ring_plan(int bm, int64_t M, int64_t I, int64_t K) {
   GatedPlan best{bm, 1, fixed + (double)rounds * pair[k] * (double)pairs + 4.2 * (double)(rounds - 1)};
   for (int64_t S = 2; S <= 16 && S <= pairs && tiles * S <= kCUs; ++S) {
     const int64_t run = (pairs + S - 1) / S, used = (pairs + run - 1) / run;
-    const double rows = M < bm ? (double)M / bm : 1.0;
-    const double t = fixed + pair[k] * (double)run + 2.0 + each[k] * rows * (double)used;
+    // of the partials' cost half goes by the rows that a tile has
+    const double rows = M < bm ? 0.5 + 0.5 * (double)M / bm : 1.0;
+    const double batch = bm == 16 && used > 8 ? 1.0 : 0.0;  // beyond the eight that are loaded at once
+    const double t = fixed + pair[k] * (double)run + 2.0 + each[k] * rows * (double)used + batch;
     if (t < best.time) best = GatedPlan{bm, used, t};
   }
   return best;
@@ -224,7 +229,10 @@ dg_status gated(const Problem& p, const Epilogue& ep, hipStream_t stream) {
     return p.K / kKBlock >= kLongKB ? launch_pipe_gated<PipeCfg<128, 256, 12>>(p, ep, stream)
                                     : launch_pipe_gated<PipeCfg<128, 256>>(p, ep, stream);
   }
-  print_dense_choice(p.M, p.N, p.K, pl.bm == 16 ? "gated_m16" : pl.bm == 32 ? "gated_m32" : "gated_m64", " (gated)");
+  char note[32];
+  snprintf(note, sizeof note, " (gated, %d K splits)", (int)pl.S);
+  print_dense_choice(p.M, p.N, p.K, pl.bm == 16 ? "gated_m16" : pl.bm == 32 ? "gated_m32" : "gated_m64",
+                     pl.S > 1 ? note : " (gated)");
   if (p.M <= pl.bm && p.N * p.K >= kGatedStreamB)
     return p.sfa_packed ? launch_gated_ring<true, true>(pl.bm, pl.S, p, ep, stream)
                         : launch_gated_ring<false, true>(pl.bm, pl.S, p, ep, stream);
