@@ -182,6 +182,13 @@ struct Workspace {
 std::mutex g_ws_mu;
 std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
 
+// What a stream's buffers are found by: its handle, but for hipStreamPerThread, one handle that
+// names another stream in every thread, the calling thread's own address.
+hipStream_t buffer_key(hipStream_t stream) {
+  thread_local char own;
+  return stream == hipStreamPerThread ? (hipStream_t)(void*)&own : stream;
+}
+
 dg_status grow(Workspace& w, void** buf, size_t* have, size_t need, size_t elem,
                hipStream_t stream, bool zero) {
   if (*have >= need) return DG_OK;
@@ -268,7 +275,7 @@ dg_status get_workspace(hipStream_t stream, size_t partial_bytes, size_t counter
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", take_error(e));
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace& w = g_ws[std::make_pair(dev, stream)];
+  Workspace& w = g_ws[std::make_pair(dev, buffer_key(stream))];
   dg_status st = grow(w, &w.partials, &w.partial_bytes, partial_bytes, 1, stream, false);
   if (st != DG_OK) return st;
   st = grow(w, (void**)&w.counters, &w.counter_count, counters, sizeof(uint32_t), stream, true);
@@ -287,7 +294,7 @@ dg_status get_transpose_workspace(hipStream_t stream, size_t a_bytes, size_t b_b
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail(DG_ERR_NO_DEVICE, "hipGetDevice: %s", take_error(e));
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace& w = g_ws[std::make_pair(dev, stream)];
+  Workspace& w = g_ws[std::make_pair(dev, buffer_key(stream))];
   dg_status st = grow(w, &w.a_t, &w.a_t_bytes, a_bytes, 1, stream, false);
   if (st != DG_OK) return st;
   st = grow(w, &w.b_t, &w.b_t_bytes, b_bytes, 1, stream, false);

@@ -30,9 +30,10 @@
  *      - transposed operand copies, for the NN / TN / TT calls;
  *      - fp32 partial column sums (in the partial tiles' buffer), for the backward calls.
  *    Calls on one stream share them in stream order, also where several threads make
- *    them at once; calls on different streams never share them. The buffers only grow. An outgrown buffer is retired, not
- *    freed: it stays allocated until dg_release_workspaces() or the end of the
- *    process, so a HIP graph captured before the growth still finds its buffers.
+ *    them at once; calls on different streams never share them (hipStreamPerThread is
+ *    another stream in every thread). The buffers only grow. An outgrown buffer is
+ *    retired, not freed: it stays allocated until dg_release_workspaces() or the end of
+ *    the process, so a HIP graph captured before the growth still finds its buffers.
  *  - HIP graph capture: a call that needs no larger buffer allocates nothing, so a
  *    call may be captured once the same shape (or a larger one) has run on that
  *    stream outside capture. A call that would have to grow a buffer while its
