@@ -1,9 +1,10 @@
 """Python binding of libdg.so, the MI355X (gfx950) FP8 block-scaled GEMM library.
 
 Argument marshalling only (of the newer calls natively, csrc/marshal.cpp, where it is
-built): every call checks dtypes, devices, shapes and contiguity, then passes raw device pointers and torch's
-current HIP stream to the C ABI declared in ``include/dg.h``. All arithmetic runs in the
-library's HIP kernels; there is no fallback path. If libdg.so is missing the import fails.
+built): every call checks dtypes, devices, shapes and contiguity, then passes raw device
+pointers and torch's current HIP stream to the C ABI declared in ``include/dg.h``. All
+arithmetic runs in the library's HIP kernels; there is no fallback path. If libdg.so is
+missing the import fails.
 
 Calls (DeepGEMM project page, aiproducthub.cn, "quick start"; DeepGEMM launch
 article, deepseek.csdn.net, section 4.2 "advanced tuning"):
@@ -595,8 +596,8 @@ def bias_act_backward_fp8(dc, pre=None, activation=None, codes=None, sf=None, db
 
 # The calls below first go through csrc/marshal.cpp, which returns None, without having called the
 # library, unless every argument is as the call wants it and on the current GPU; the Python code
-# behind it then raises the specific error, or makes the call on another GPU. (layernorm_fp8_1x128 of one row takes the host 8.4 us
-# through Python's checks.)
+# behind it then raises the specific error, or makes the call on another GPU. (layernorm_fp8_1x128
+# of one row takes the host 8.4 us through Python's checks.)
 
 def _rng(rng, x: torch.Tensor, index: int):
     """rng's address: int64 [2] on x's GPU, (seed, offset); None without one."""
